@@ -32,3 +32,16 @@ from ._binding import (  # noqa: F401
     dist_gemm_step_timeline,
     lib,
 )
+from ._mx import (  # noqa: F401
+    ELEMS,
+    MX_C_FUNCTIONS,
+    MX_FORMATS,
+    NORM_OUTPUTS,
+    MxPlan,
+    dist_gemm_mx_dequantize,
+    dist_gemm_mx_quantize,
+    dist_gemm_mx_scale_pitch,
+    dist_gemm_rms_norm,
+    dist_gemm_rms_norm_backward,
+    dist_gemm_rms_norm_workspace,
+)

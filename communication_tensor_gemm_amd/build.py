@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libdistgemm.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["gemm_mfma16.hip", "gemm_mfma_f8.hip", "distgemm.hip"]
+SOURCES = ["gemm_mfma16.hip", "gemm_mfma_f8.hip", "distgemm.hip", "mx_quant.hip", "rms_norm.hip",
+           "mx_gemm_rows.hip", "mx_api.hip"]
 # per-source extra flags
 EXTRA = {
     # the fp32 half slab is 256 MFMAs long; without a higher threshold the

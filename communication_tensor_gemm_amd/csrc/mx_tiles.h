@@ -1,0 +1,153 @@
+// Device helpers of the MX product kernels: buffer loads, the groups' tile
+// search and the element epilogue.
+#pragma once
+#include "mx_common.h"
+
+namespace dg {
+namespace mx {
+
+typedef __attribute__((ext_vector_type(4))) int i32x4;
+typedef __attribute__((ext_vector_type(8))) int i32x8;
+
+constexpr uint32_t kOutOfRange = 0x80000000u;  // an offset past every descriptor's end: the load gives zeros
+
+// Buffer descriptor of a wave-uniform base and byte count (below 2^31).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), (short)0,
+                                           static_cast<int>(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000);
+}
+
+__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff = 0) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
+}
+
+// The rows of one group tile.
+struct GroupTile {
+  int32_t group;  // -1: there is no such tile
+  int32_t row0;   // first row of the tile
+  int32_t rows;   // rows left in the group from there
+  int32_t index;  // the tile's place in the group, of `tiles`
+  int32_t tiles;
+};
+
+// Row tile u (of height tm) of the groups' rows, groups in order, each with
+// ceil(rows / tm) tiles.  Offsets are clamped to [0, M] and to be ascending,
+// so that wrong ones cannot reach past the operands.  The wave's 64 lanes
+// take 64 groups at a time: a scan of their tile counts, then a ballot.
+// Every lane of the wave calls it with the same arguments.  total: all tiles.
+__device__ __forceinline__ int32_t group_bound(const int32_t* offsets, int32_t i, int32_t M) {
+  return min(max(offsets[i], 0), M);
+}
+
+__device__ __forceinline__ GroupTile find_group_tile(const int32_t* offsets, int32_t groups, int32_t M, int32_t tm,
+                                                     int32_t u) {
+  const int lane = threadIdx.x & 63;
+  int32_t before = 0;  // tiles of the groups already passed
+  for (int32_t base = 0; base < groups; base += 64) {
+    const int32_t g = base + lane;
+    int32_t lo = 0, hi = 0;
+    if (g < groups) {
+      lo = group_bound(offsets, g, M);
+      hi = max(lo, group_bound(offsets, g + 1, M));
+    }
+    const int32_t n = (hi - lo + tm - 1) / tm;
+    int32_t incl = n;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int32_t v = __shfl_up(incl, s);
+      if (lane >= s) incl += v;
+    }
+    const uint64_t past = __ballot(before + incl > u);
+    if (past != 0) {
+      const int first = __builtin_ctzll(past);
+      GroupTile t;
+      const int32_t n1 = __builtin_amdgcn_readlane(n, first), i1 = __builtin_amdgcn_readlane(incl, first);
+      const int32_t lo1 = __builtin_amdgcn_readlane(lo, first), hi1 = __builtin_amdgcn_readlane(hi, first);
+      t.group = base + first;
+      t.tiles = n1;
+      t.index = u - (before + i1 - n1);
+      t.row0 = lo1 + t.index * tm;
+      t.rows = hi1 - t.row0;
+      return t;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return GroupTile{-1, 0, 0, 0, 0};
+}
+
+// All row tiles of height tm.
+__device__ __forceinline__ int32_t count_group_tiles(const int32_t* offsets, int32_t groups, int32_t M, int32_t tm) {
+  const int lane = threadIdx.x & 63;
+  int32_t n = 0;
+  for (int32_t g = lane; g < groups; g += 64) {
+    const int32_t lo = group_bound(offsets, g, M), hi = max(lo, group_bound(offsets, g + 1, M));
+    n += (hi - lo + tm - 1) / tm;
+  }
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) n += __shfl_xor(n, s);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Row tiles that `groups` groups with M rows together can have at most.
+inline int64_t most_group_tiles(int64_t M, int64_t groups, int64_t tm) {
+  const int64_t some = groups < M ? groups : M;  // groups that can have a row
+  return some + (M - some) / tm;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float load_value(const void* p, int64_t i) {
+  if constexpr (kBf16)
+    return __builtin_bit_cast(float, static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+  else
+    return static_cast<const float*>(p)[i];
+}
+
+// Four neighbouring values of row `row` from column `col`: alpha * v + beta *
+// C + bias, rounded once.  n values are inside D; wide: the row's 4-element
+// pieces are aligned for one store.
+template <bool kBf16>
+__device__ __forceinline__ void store_four(const MxGemmArgs& a, int64_t bias0, int64_t row, int32_t col, int32_t n,
+                                           bool wide, f32x4 v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float o = a.alpha * v[e];
+    if (e < n) {
+      if (a.beta != 0.0f) o = __builtin_fmaf(a.beta, load_value<kBf16>(a.C, row * a.ldc + col + e), o);
+      if (a.bias) o += load_value<kBf16>(a.bias, bias0 + col + e);
+    }
+    v[e] = o;
+  }
+  const int64_t at = row * a.ldd + col;
+  if constexpr (kBf16) {
+    uint16_t* d = static_cast<uint16_t*>(a.D) + at;
+    if (wide && n >= 4) {
+      *reinterpret_cast<u32x2*>(d) = u32x2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) d[e] = static_cast<uint16_t>(bf16_rne(v[e]));
+    }
+  } else {
+    float* d = static_cast<float*>(a.D) + at;
+    if (wide && n >= 4) {
+      *reinterpret_cast<f32x4*>(d) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) d[e] = v[e];
+    }
+  }
+}
+
+// Whether D's rows allow a store of four values at once.
+template <bool kBf16>
+__device__ __forceinline__ bool wide_rows(const MxGemmArgs& a) {
+  constexpr uint64_t es = kBf16 ? 2 : 4;
+  return ((reinterpret_cast<uint64_t>(a.D) | static_cast<uint64_t>(a.ldd) * es) & (4 * es - 1)) == 0;
+}
+
+}  // namespace mx
+}  // namespace dg
