@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libdistgemm.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["gemm_mfma16.hip", "gemm_mfma_f8.hip", "distgemm.hip", "mx_quant.hip", "rms_norm.hip",
-           "mx_gemm_rows.hip", "mx_api.hip"]
+           "mx_gemm_rows.hip", "mx_gemm_tile.hip", "mx_api.hip"]
 # per-source extra flags
 EXTRA = {
     # the fp32 half slab is 256 MFMAs long; without a higher threshold the
@@ -26,6 +26,8 @@ EXTRA = {
     "gemm_mfma16.hip": ["-mllvm", "-pragma-unroll-threshold=1000000"],
     # same guard for the fp8 unit's fully unrolled slab and epilogue
     "gemm_mfma_f8.hip": ["-mllvm", "-pragma-unroll-threshold=1000000"],
+    # and for the MX tiles
+    "mx_gemm_tile.hip": ["-mllvm", "-pragma-unroll-threshold=1000000"],
 }
 ARCH = "gfx950"
 

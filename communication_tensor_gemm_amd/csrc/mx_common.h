@@ -98,6 +98,8 @@ hipError_t launch_rms_norm(int type, int out, const NormArgs& a, hipStream_t st)
 int64_t rms_norm_backward_blocks(int64_t rows, int64_t cols);
 hipError_t launch_rms_norm_backward(int type, const NormBackwardArgs& a, hipStream_t st);
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t st);
+// on tiles of `size` (256 or 128) squared
+hipError_t launch_mx_gemm_tile(int size, const MxGemmArgs& a, hipStream_t st);
 
 // Largest row that the RMS norm kernels keep in registers.
 constexpr int kNormMaxCols = 32768;

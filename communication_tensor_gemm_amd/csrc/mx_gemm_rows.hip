@@ -171,12 +171,15 @@ static hipError_t rows_t(const MxGemmArgs& a, hipStream_t st) {
 
 }  // namespace mx
 
+// Few rows stream the weights; from 65 rows on (of a group, on average), tiles.
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t st) {
-  if (a.M == 0 || (a.offsets && a.groups == 0)) return hipSuccess;
-  const int64_t rows = a.offsets ? a.M / a.groups : a.M;  // of a group, on average
+  if (a.M == 0) return hipSuccess;
+  const int64_t rows = a.offsets ? a.M / a.groups : a.M;
   if (rows <= 16) return mx::rows_t<1, 1>(a, st);
   if (rows <= 32) return mx::rows_t<2, 2>(a, st);
-  return mx::rows_t<4, 2>(a, st);
+  if (rows <= 64) return mx::rows_t<4, 2>(a, st);
+  const int64_t tiles = ((rows + 255) / 256) * ((a.N + 255) / 256) * (a.offsets ? a.groups : 1);
+  return launch_mx_gemm_tile(tiles >= 192 ? 256 : 128, a, st);
 }
 
 }  // namespace dg
