@@ -61,7 +61,7 @@ int check_mx(const void* plain, int64_t ld, int elem, int64_t rows, int64_t cols
 struct dist_gemm_mx_plan_s {
   int64_t M = 0, N = 0, K = 0, groups = 0;
   int a_format = 0, out_elem = 0;
-  int device = 0;
+  int device = 0, cus = 256;
   std::string err = "no error";
 };
 
@@ -179,10 +179,11 @@ int dist_gemm_mx_plan(int64_t M, int64_t N, int64_t K, int64_t groups, int a_for
   dist_gemm_mx_plan_s* p = new (std::nothrow) dist_gemm_mx_plan_s;
   if (!p) return fail(nullptr, DIST_GEMM_ERR_OOM, "no host memory for the plan");
   p->M = M; p->N = N; p->K = K; p->groups = groups; p->a_format = a_format; p->out_elem = out_elem;
-  const hipError_t e = hipGetDevice(&p->device);
+  hipError_t e = hipGetDevice(&p->device);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&p->cus, hipDeviceAttributeMultiprocessorCount, p->device);
   if (e != hipSuccess) {
     delete p;
-    return hip_status(nullptr, e, "hipGetDevice");
+    return hip_status(nullptr, e, "device query");
   }
   *out = p;
   return DIST_GEMM_OK;
@@ -217,6 +218,7 @@ int dist_gemm_mx_run(dist_gemm_mx_plan_t P, int64_t rows, const void* A, const v
   a.M = static_cast<int32_t>(rows); a.N = static_cast<int32_t>(P->N); a.K = static_cast<int32_t>(P->K);
   a.groups = static_cast<int32_t>(P->groups);
   a.a_format = P->a_format; a.out_bf16 = P->out_elem == DIST_GEMM_ELEM_BF16;
+  a.cus = P->cus;
   a.alpha = alpha; a.beta = beta;
   int prev = P->device;
   (void)hipGetDevice(&prev);

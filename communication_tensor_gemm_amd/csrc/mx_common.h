@@ -89,6 +89,7 @@ struct MxGemmArgs {
   int32_t groups;     // 0: no groups
   int32_t a_format;
   int32_t out_bf16;
+  int32_t cus;        // CUs of the device
   float alpha, beta;
 };
 
@@ -112,18 +113,27 @@ typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((ext_vector_type(4))) unsigned int u32x4;
 typedef __attribute__((ext_vector_type(2))) unsigned int u32x2;
 typedef __attribute__((ext_vector_type(2))) short s16x2;
+// the same at any alignment of their element: still one access of full width
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
 
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-  uint32_t u = __builtin_bit_cast(uint32_t, f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;  // quiet NaN
-  return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+// Two values rounded to bf16 (to nearest even, a NaN stays one), the first
+// low: one v_cvt_pk_bf16_f32, where integer rounding takes 14 instructions (the
+// norm's gradient is bound by such instructions as much as by memory).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
-// Eight consecutive elements of a row, as loaded.  n < 8 (unaligned path
-// only): elements past the row's end read as zero.
+// Eight consecutive elements of a row, as loaded.  Not kAligned: addresses
+// are aligned to the element only, and a piece may have n < 8 elements left
+// in its row (those past the end read as zero); whole pieces still move in
+// accesses of full width (a 1021 x 5123 fp32 norm, whose rows start on every
+// 4-byte offset: 31 us with element accesses, 14 us with these).
 template <int T>
 struct Raw8;
 template <>
@@ -134,6 +144,8 @@ struct Raw8<PT_BF16> {
     const uint16_t* s = static_cast<const uint16_t*>(p) + i;
     if constexpr (kAligned) {
       w = *reinterpret_cast<const u32x4*>(s);
+    } else if (n >= 8) {
+      w = *reinterpret_cast<const u32x4_any*>(s);
     } else {
       uint32_t e[8];
 #pragma unroll
@@ -153,7 +165,7 @@ struct Raw8<PT_BF16> {
   // round to the type; f keeps the rounded values
   __device__ __forceinline__ void set(float (&f)[8]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = bf16_rne(f[2 * j]) | (bf16_rne(f[2 * j + 1]) << 16);
+    for (int j = 0; j < 4; ++j) w[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
     get(f);
   }
   template <bool kAligned>
@@ -161,6 +173,8 @@ struct Raw8<PT_BF16> {
     uint16_t* d = static_cast<uint16_t*>(p) + i;
     if constexpr (kAligned) {
       *reinterpret_cast<u32x4*>(d) = w;
+    } else if (n >= 8) {
+      *reinterpret_cast<u32x4_any*>(d) = w;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -177,6 +191,9 @@ struct Raw8<PT_F32> {
     if constexpr (kAligned) {
       a = *reinterpret_cast<const f32x4*>(s);
       b = *reinterpret_cast<const f32x4*>(s + 4);
+    } else if (n >= 8) {
+      a = *reinterpret_cast<const f32x4_any*>(s);
+      b = *reinterpret_cast<const f32x4_any*>(s + 4);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -206,6 +223,9 @@ struct Raw8<PT_F32> {
     if constexpr (kAligned) {
       *reinterpret_cast<f32x4*>(d) = a;
       *reinterpret_cast<f32x4*>(d + 4) = b;
+    } else if (n >= 8) {
+      *reinterpret_cast<f32x4_any*>(d) = a;
+      *reinterpret_cast<f32x4_any*>(d + 4) = b;
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

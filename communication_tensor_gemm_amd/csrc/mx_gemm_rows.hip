@@ -94,14 +94,16 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemm_rows_kernel(MxGemmArgs a)
       sa[i] = load16(rAs, oas[i], k0 / kMxBlock);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u) {
+      // a scale byte past K may hold anything, also the NaN scale
+      const bool in = !kLast || k0 + 128 * u + 32 * q < a.K;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const i32x8 vb = {fb[j][u][0], fb[j][u][1], fb[j][u][2], fb[j][u][3], 0, 0, 0, 0};
-        const int vsb = static_cast<int>(static_cast<uint32_t>(sb[j][u]) >> (8 * q));
+        const int vsb = in ? static_cast<int>(static_cast<uint32_t>(sb[j][u]) >> (8 * q)) : 0;
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-          const int vsa = static_cast<int>(static_cast<uint32_t>(sa[i][u]) >> (8 * q));
+          const int vsa = in ? static_cast<int>(static_cast<uint32_t>(sa[i][u]) >> (8 * q)) : 0;
           if constexpr (A8) {
             const i32x4 lo = fa[i][2 * u], hi = fa[i][2 * u + 1];
             const i32x8 va = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -112,6 +114,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemm_rows_kernel(MxGemmArgs a)
           }
         }
       }
+    }
   };
   const int whole = a.K / kChunk;
   for (int c = wave; c < whole; c += kWaves) step(c, std::false_type{});

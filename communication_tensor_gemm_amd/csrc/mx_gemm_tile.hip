@@ -8,21 +8,32 @@
 //
 // K is walked in slabs of 128 bytes per row of A: 256 elements of E2M1 (128
 // bytes per row of B too) or 128 of E4M3 (64 bytes per row of B), each in two
-// half slabs.  Slabs go from memory straight into LDS (buffer_load_dwordx4
-// ... lds, 1 KiB per wave instruction, whole rows of the slab), two stages of
-// E2M1 or three of E4M3; the scales in chunks of 512 elements (16 bytes per
-// row), two buffers.  While a half slab is multiplied from one set of
-// registers, the next is read from LDS into the other; one barrier per slab
-// says that every wave has read its second half, which frees the slab's
-// stage for the loads of the slab two (E4M3: three) further on.
+// halves.  Slabs go from memory straight into LDS (buffer_load_dwordx4 ...
+// lds, 1 KiB per wave instruction, whole lines of 128 bytes where the rows
+// allow it: slabs of 64 bytes per row, twice as many of them, measured 13%
+// slower), two stages of E2M1 or three of E4M3; the scales in chunks of 512
+// elements (16 bytes per row), two buffers.  While half a slab is multiplied
+// from one set of registers, the next half is read from LDS into the other.
+// One barrier per slab, between its halves, says that every wave has read
+// the second half, which frees the slab's stage for the loads of the slab two
+// (E4M3: three) further on, and that the next slab has landed.  MFMAs, reads
+// and loads alternate in a fixed order (scheduling barriers keep it).  The
+// scales' loads touch a line per lane, so they are placed in the half without
+// other loads.
 //
-// Operand layout (see mx_gemm_rows.hip for the MFMA's): lane l has row l % 32
-// and, with h = l / 32, an E2M1 block of 32 elements, or of E4M3 elements 16 h
-// .. + 15 and 32 + 16 h .. + 15 of 64.  E2M1 x E2M1 takes the K order freely
-// (both operands alike): half h of the lanes works on the h-th 128 elements of
-// the slab, so that the four MFMAs of a slab use the four bytes of one dword
-// of scales per lane, by op_sel.  With E4M3 the order is fixed inside 64, and
-// the lane's dword of scales (four blocks, a slab) is shifted by h bytes once.
+// Tile boundaries.  The launch is persistent: a workgroup's slabs form one
+// stream over all of its tiles, and the loads, reads and scales of the next
+// tile's first slabs are issued during the current tile's last ones, so a
+// tile begins without waiting.  Its first MFMAs take 0 for their C operand.
+// With one workgroup per CU, prologue and epilogue of a tile took 18 us of
+// 127 (E2M1, K = 16384) when nothing overlapped them.
+//
+// Operand layout (see mx_gemm_rows.hip for the other MFMA's): lane l has row
+// l % 32 and, with h = l / 32, an E2M1 block of 32 elements, or of E4M3
+// elements 16 h .. + 15 and 32 + 16 h .. + 15 of 64.  Its scale is that of
+// block h of the 64, in both cases: of a dword of scales (four blocks, 128
+// elements), byte h for the first 64 and 2 + h for the second, so the dword is
+// shifted by h bytes once and op_sel takes bytes 0 and 2.
 //
 // LDS layout.  128-byte rows: blocks of 8 rows (1 KiB), half row s at + 512 s,
 // row r at + 64 (r % 8), 16-byte piece q of the half at + 16 (q ^ f(r)), f(r) =
@@ -30,18 +41,18 @@
 // on distinct banks.  64-byte rows: blocks of 16 rows, the same with one half.
 //
 // K past the end (K is a multiple of 32, not of the slab): the lanes whose
-// piece of the last slab lies past K get an out-of-range offset once, before
-// that slab's loads, and receive zeros; all earlier slabs are loaded unmasked.
+// piece of the last slab lies past K get an out-of-range offset for that
+// slab's loads, and receive zeros; all other slabs are loaded unmasked.
 #include "mx_tiles.h"
 
 namespace dg {
 namespace mx {
 
 typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(2))) int i32x2;
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int kXcds = 8;
-constexpr int kChunkK = 512;  // elements of K per chunk of scales
 
 __device__ __forceinline__ int row_perm(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
 
@@ -57,28 +68,26 @@ __device__ __forceinline__ void barrier_only() { asm volatile("s_barrier" ::: "m
 // acc += B block x A block, the scales' byte J of both dwords.  Inline asm
 // with the accumulator tied to its AGPRs: the builtin's accumulators are
 // copied between MFMAs when all 256 are in use.
+#define DG_MX_MFMA(SELHI, FORMATS)                                                                               \
+  asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:" SELHI " " FORMATS \
+               : "+a"(acc)                                                                                       \
+               : "v"(b), "v"(a), "v"(sb), "v"(sa))
 template <int J>
 __device__ __forceinline__ void mfma(f32x16& acc, const i32x4& b, const i32x4& a, int sb, int sa) {
-#define DG_MX_MFMA(SEL, SELHI, FORMATS)                                                                              \
-  asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:" SEL " op_sel_hi:" SELHI " " FORMATS \
-               : "+a"(acc)                                                                                           \
-               : "v"(b), "v"(a), "v"(sb), "v"(sa))
-#define DG_MX_MFMA_BYTE(FORMATS)                       \
-  if constexpr (J == 0)                                \
-    DG_MX_MFMA("[0,0,0]", "[0,0,0]", FORMATS);         \
-  else if constexpr (J == 1)                           \
-    DG_MX_MFMA("[1,1,0]", "[0,0,0]", FORMATS);         \
-  else if constexpr (J == 2)                           \
-    DG_MX_MFMA("[0,0,0]", "[1,1,0]", FORMATS);         \
-  else                                                 \
-    DG_MX_MFMA("[1,1,0]", "[1,1,0]", FORMATS)
-  DG_MX_MFMA_BYTE("cbsz:4 blgp:4");
+  static_assert(J == 0 || J == 2, "scale byte");
+  if constexpr (J == 0)
+    DG_MX_MFMA("[0,0,0]", "cbsz:4 blgp:4");
+  else
+    DG_MX_MFMA("[1,1,0]", "cbsz:4 blgp:4");
 }
 template <int J>
 __device__ __forceinline__ void mfma(f32x16& acc, const i32x4& b, const i32x8& a, int sb, int sa) {
-  DG_MX_MFMA_BYTE("cbsz:4");
+  static_assert(J == 0 || J == 2, "scale byte");
+  if constexpr (J == 0)
+    DG_MX_MFMA("[0,0,0]", "cbsz:4");
+  else
+    DG_MX_MFMA("[1,1,0]", "cbsz:4");
 }
-#undef DG_MX_MFMA_BYTE
 #undef DG_MX_MFMA
 
 template <bool A8, int NBM, int NBN>
@@ -87,113 +96,265 @@ struct Geo {
   static constexpr int TM = 64 * NBM, TN = 64 * NBN;
   static constexpr int kSlabK = A8 ? 128 : 256;
   static constexpr int kRowB = A8 ? 64 : 128;  // bytes of a row of B per slab
-  static constexpr int SA = TM * 128, SB = TN * kRowB;
+  static constexpr int SA = TM * 128, SB = TN * kRowB, kStage = SA + SB;
   static constexpr int kStages = A8 ? 3 : 2;
   static constexpr int kScales = (TM + TN) * 16;
-  static constexpr int kLds = kStages * (SA + SB) + 2 * kScales;
+  static constexpr int kLds = kStages * kStage + 2 * kScales;
   static constexpr int LA = SA / 4096, LB = SB / 4096, LS = kScales / 4096;  // loads per wave
-  static constexpr int kPerChunk = kChunkK / kSlabK;                         // slabs per chunk of scales
+  static constexpr int kPerChunk = 512 / kSlabK;                             // slabs per chunk of scales
   static constexpr int kSteps = A8 ? 1 : 2;                                  // MFMAs of a block per half slab
+  static constexpr int kWgs = NBM * NBN == 16 ? 1 : 2;                       // workgroups per CU
+  static constexpr int kStores = NBM * NBN * 2;                              // of a whole bf16 wave block
 };
 
-// One tile: rows row0 .. + rows_left of A (and D), columns n0 .. of the B at
-// row b_row0 + n0.  Every argument is workgroup-uniform.
+// One tile's place.
+struct Place {
+  int32_t row0, rows;  // first row of A and D, rows from there on (0: no tile)
+  int32_t n0, cols;
+  int64_t b_row0;      // row of B that holds its group's column 0
+};
+
+// Height, in tiles, of a band of tile rows that is walked column by column.
+constexpr int kBand = 4;
+
+// Place w of the order of a tiles_m x tiles_n grid.
+__device__ __forceinline__ void order_tile(int32_t w, int32_t tiles_m, int32_t tiles_n, int32_t& tm, int32_t& tn) {
+  const int32_t band = w / (kBand * tiles_n), first = band * kBand;
+  const int32_t high = min(kBand, tiles_m - first), in = w - band * kBand * tiles_n;
+  tm = first + in % high;
+  tn = in / high;
+}
+
+// The tiles of a launch in their order: workgroup b runs on XCD b mod 8, and
+// each XCD takes one contiguous range of the order, its workgroups in turn.
+struct Tiles {
+  int32_t tiles_n, row_tiles, begin, end, step;
+  GroupLanes groups;
+};
+
+// The launch's arguments read again where they are needed (scalar loads from
+// the kernel's argument segment, which starts with them): held over the main
+// loop they, and what the compiler derives from them ahead of it, would push
+// the loop's own scalars out of the SGPRs.
+__device__ __forceinline__ MxGemmArgs fresh_args() {
+  typedef __attribute__((address_space(4))) const uint32_t* words_t;
+  words_t q = (words_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(q));
+  struct Words {
+    uint32_t w[sizeof(MxGemmArgs) / 4];
+  } a;
+  static_assert(sizeof(MxGemmArgs) % 4 == 0, "whole words");
+#pragma unroll
+  for (size_t i = 0; i < sizeof(MxGemmArgs) / 4; ++i) a.w[i] = q[i];
+  return __builtin_bit_cast(MxGemmArgs, a);
+}
+
+template <typename G>
+__device__ __forceinline__ Tiles all_tiles(const MxGemmArgs& p) {
+  Tiles t;
+  t.tiles_n = (p.N + G::TN - 1) / G::TN;
+  if (p.offsets) {
+    t.groups = load_groups(p.offsets, p.groups, p.M, G::TM);
+    t.row_tiles = p.groups <= 64 ? __builtin_amdgcn_readlane(t.groups.incl, 63)
+                                 : count_group_tiles(p.offsets, p.groups, p.M, G::TM);
+  } else {
+    t.row_tiles = (p.M + G::TM - 1) / G::TM;
+  }
+  const int32_t T = t.row_tiles * t.tiles_n;
+  const int32_t x = static_cast<int32_t>(blockIdx.x) % kXcds, each = T / kXcds, more = T % kXcds;
+  t.begin = x * each + min(x, more) + static_cast<int32_t>(blockIdx.x) / kXcds;
+  t.end = (x + 1) * each + min(x + 1, more);
+  t.step = static_cast<int32_t>(gridDim.x) / kXcds;
+  return t;
+}
+
+template <typename G>
+__device__ __forceinline__ Place place_of(Tiles t, int32_t at) {
+  const MxGemmArgs p = fresh_args();
+  asm volatile("" : "+s"(t.tiles_n), "+s"(t.row_tiles));  // nothing of the divisions ahead of the loop either
+  Place q{0, 0, 0, 0, 0};
+  if (at >= t.end) return q;
+  int32_t tm, tn, row0 = 0, rows = p.M;
+  if (p.offsets) {
+    const int32_t u = at / t.tiles_n;
+    const GroupTile g = p.groups <= 64 ? group_tile_of(t.groups, 0, 0, G::TM, u)
+                                       : find_group_tile(p.offsets, p.groups, p.M, G::TM, u);
+    if (g.group < 0) return q;
+    // the group's tiles are a grid of their own, from its first row tile on
+    row0 = g.row0 - g.index * G::TM;
+    rows = g.rows + g.index * G::TM;
+    q.b_row0 = static_cast<int64_t>(g.group) * p.N;
+    order_tile(at - (u - g.index) * t.tiles_n, g.tiles, t.tiles_n, tm, tn);
+  } else {
+    order_tile(at, t.row_tiles, t.tiles_n, tm, tn);
+  }
+  q.row0 = row0 + tm * G::TM;
+  q.rows = min(rows - tm * G::TM, G::TM);
+  q.n0 = tn * G::TN;
+  q.cols = min(p.N - q.n0, G::TN);
+  return q;
+}
+
+// The wave's block of D from its accumulators.  A lane holds, of block (i,
+// j), row l % 32 and columns 8 g + 4 h + 0 .. 3 (g = 0 .. 3).  A whole bf16
+// block without C: the two halves of the wave exchange their fours of g and
+// g + 1, so that each lane has eight neighbouring columns and an instruction
+// stores 32 rows of 32 bytes (kStores instructions in all, and true is
+// returned); else four columns at a time.  No LDS: the next tile's slabs are
+// in it.
+template <bool kBf16, int NBM, int NBN>
+__device__ __forceinline__ bool store_block_of(const MxGemmArgs& p, const Place& at, int wm, int wn, int lane,
+                                               f32x16 (&acc)[NBM][NBN]) {
+  constexpr int WM = 32 * NBM, WN = 32 * NBN;
+  const int32_t wrow = wm * WM, wcol = wn * WN;
+  const bool whole = kBf16 && at.rows - wrow >= WM && at.cols - wcol >= WN && p.beta == 0.0f &&
+                     ((reinterpret_cast<uint64_t>(p.D) | (static_cast<uint64_t>(p.ldd) * 2)) & 15) == 0;
+  const bool wide = wide_rows<kBf16>(p);
+#pragma unroll
+  for (int i = 0; i < NBM; ++i)
+#pragma unroll
+    for (int j = 0; j < NBN; ++j) {
+      // one block at a time, its addresses from a lane index of its own, so that
+      // nothing is computed ahead for all of them: the registers hold the loop's state
+      __builtin_amdgcn_sched_barrier(0);
+      int l = lane;
+      asm volatile("" : "+v"(l));
+      asm volatile("" : "+a"(acc[i][j]));
+      const int el = l & 31, eh = l >> 5;
+      const int32_t r = wrow + 32 * i + el, c0 = wcol + 32 * j;
+      if (whole) {
+        u32x2 w[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = p.alpha * acc[i][j][4 * g + e];
+          if (p.bias) {  // N values per group, as B's rows
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += load_value<true>(p.bias, at.b_row0 + at.n0 + c0 + 8 * g + 4 * eh + e);
+          }
+          w[g] = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        }
+        const auto d = (global_ptr<uint16_t>)p.D + static_cast<int64_t>(at.row0 + r) * p.ldd + at.n0 + c0 + 8 * eh;
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+          // the upper half's fours of g against the lower half's of g + 1
+          const auto x = __builtin_amdgcn_permlane32_swap(w[g][0], w[g + 1][0], false, false);
+          const auto y = __builtin_amdgcn_permlane32_swap(w[g][1], w[g + 1][1], false, false);
+          *(global_ptr<u32x4>)(d + 8 * g) = u32x4{x[0], y[0], x[1], y[1]};
+        }
+      } else if (r < at.rows) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int32_t c = c0 + 8 * g + 4 * eh;
+          if (c < at.cols)
+            store_four<kBf16>(p, at.b_row0, at.row0 + r, at.n0 + c, at.cols - c, wide,
+                              f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]});
+        }
+      }
+    }
+  return whole;
+}
+
+// A workgroup's share of the launch.
 template <bool A8, bool kBf16, int NBM, int NBN>
-__device__ __forceinline__ void mx_tile(const MxGemmArgs& p, int32_t row0, int32_t rows_left, int32_t n0,
-                                        int64_t b_row0, uint8_t* smem) {
+__device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* smem) {
   using G = Geo<A8, NBM, NBN>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, h = lane >> 5;
-  const int32_t rows = min(rows_left, G::TM), cols = min(p.N - n0, G::TN);
-  const uint32_t lda = static_cast<uint32_t>(A8 ? p.K : p.K / 2), ldb = static_cast<uint32_t>(p.K / 2);
-  const uint32_t lds_pitch = static_cast<uint32_t>(scale_pitch(p.K));
-  const auto rA = make_rsrc(p.A + static_cast<int64_t>(row0) * lda, rows * lda);
-  const auto rB = make_rsrc(p.B + (b_row0 + n0) * ldb, cols * ldb);
-  // this wave loads scales of A (waves 0, 1) or of B (2, 3)
-  const bool scale_a = wave < 2;
-  const auto rS = make_rsrc(scale_a ? p.As + static_cast<int64_t>(row0) * lds_pitch : p.Bs + (b_row0 + n0) * lds_pitch,
-                            (scale_a ? rows : cols) * lds_pitch);
-  const int KT = (p.K + G::kSlabK - 1) / G::kSlabK, KC = (p.K + kChunkK - 1) / kChunkK;
+  const Tiles tiles = all_tiles<G>(p);
+  int32_t at = tiles.begin;
+  if (at >= tiles.end) return;
 
-  // loads: lane offsets.  128-byte rows: even / odd blocks of 8 rows.
-  uint32_t ga[2], gb[2];
-  {
-    const int half = lane >> 5, brow = (lane >> 2) & 7, piece = lane & 3;
-#pragma unroll
-    for (int odd = 0; odd < 2; ++odd) {
-      const int r16 = 8 * odd + brow, at = 16 * (4 * half + (piece ^ row_perm(r16)));
-      ga[odd] = (8 * G::LA * wave + r16) * lda + at;
-      if constexpr (!A8) gb[odd] = (8 * G::LB * wave + r16) * ldb + at;
-    }
-    if constexpr (A8) {
-      const int r16 = lane >> 2;
-      gb[0] = gb[1] = (16 * G::LB * wave + r16) * ldb + 16 * (piece ^ row_perm(r16));
-    }
-  }
-  const uint32_t gs = static_cast<uint32_t>((scale_a ? wave : wave - 2) * 64 * G::LS + lane) * lds_pitch;
-  // the last slab's pieces past K
+  Place cur = place_of<G>(tiles, at), next = place_of<G>(tiles, at + tiles.step);
+  const uint32_t lda = static_cast<uint32_t>(A8 ? p.K : p.K / 2), ldb = static_cast<uint32_t>(p.K / 2);
+  const uint32_t pitch = static_cast<uint32_t>(scale_pitch(p.K));
+  const int KT = (p.K + G::kSlabK - 1) / G::kSlabK, KC = (p.K + 511) / 512;
   const bool partial = KT * G::kSlabK != p.K;
-  auto mask_last = [&]() {
-    const int k0 = (KT - 1) * G::kSlabK;
-    const int half = lane >> 5, brow = (lane >> 2) & 7, piece = lane & 3;
+  uint8_t* const scales = smem + G::kStages * G::kStage;
+
+  // ---- loads.  The loader walks the workgroup's stream of slabs; lkt is its
+  // slab of the tile that rA and rB describe.  (No tile: no bytes, all zeros.)
+  __amdgpu_buffer_rsrc_t rA, rB, rS;
+  auto slabs_of = [&](const Place& q) {
+    const MxGemmArgs p = fresh_args();
+    rA = make_rsrc(p.A + static_cast<int64_t>(q.row0) * lda, q.rows * lda);
+    rB = make_rsrc(p.B + (q.b_row0 + q.n0) * ldb, q.cols * ldb);
+  };
+  // waves 0, 1 load scales of A, 2, 3 of B
+  const bool scale_a = wave < 2;
+  auto scales_of = [&](const Place& q) {
+    const MxGemmArgs p = fresh_args();
+    rS = make_rsrc(scale_a ? p.As + static_cast<int64_t>(q.row0) * pitch : p.Bs + (q.b_row0 + q.n0) * pitch,
+                   (scale_a ? q.rows : q.cols) * pitch);
+  };
+  // lane offsets: 128-byte rows in even and odd blocks of 8 rows, 64-byte rows in blocks of 16
+  const int piece = lane & 3, r16 = lane >> 2;
+  auto byte_in_slab = [&](int odd) { return 16 * (4 * (lane >> 5) + (piece ^ row_perm(8 * odd + (r16 & 7)))); };
+  uint32_t ga[2], gb[2];
+#pragma unroll
+  for (int odd = 0; odd < 2; ++odd) {
+    ga[odd] = (8 * G::LA * wave + 8 * odd + (r16 & 7)) * lda + byte_in_slab(odd);
+    gb[odd] = A8 ? (16 * G::LB * wave + r16) * ldb + 16 * (piece ^ row_perm(r16))
+                 : (8 * G::LB * wave + 8 * odd + (r16 & 7)) * ldb + byte_in_slab(odd);
+  }
+  const uint32_t gs = static_cast<uint32_t>((scale_a ? wave : wave - 2) * 64 * G::LS + lane) * pitch;
+  int lkt = 0;
+  // before the loads of slab lkt, K not a multiple of the slab: the last
+  // slab's pieces past K out of range, the first slab's back in
+  auto mask = [&]() {
+    if (!partial || (lkt != 0 && lkt != KT - 1)) return;
+    const int k0 = lkt * G::kSlabK;
+    const bool last = lkt == KT - 1;
 #pragma unroll
     for (int odd = 0; odd < 2; ++odd) {
-      const int byte = 16 * (4 * half + (piece ^ row_perm(8 * odd + brow)));
-      if (k0 + (A8 ? byte : 2 * byte) >= p.K) ga[odd] |= kOutOfRange;
-      if constexpr (!A8)
-        if (k0 + 2 * byte >= p.K) gb[odd] |= kOutOfRange;
+      const int ka = k0 + byte_in_slab(odd) * (A8 ? 1 : 2);
+      const int kb = A8 ? k0 + 32 * (piece ^ row_perm(r16)) : ka;
+      ga[odd] = (ga[odd] & ~kOutOfRange) | (last && ka >= p.K ? kOutOfRange : 0u);
+      gb[odd] = (gb[odd] & ~kOutOfRange) | (last && kb >= p.K ? kOutOfRange : 0u);
     }
-    if constexpr (A8)
-      if (k0 + 32 * (piece ^ row_perm(lane >> 2)) >= p.K) gb[0] |= kOutOfRange;
   };
-  auto stage = [&](int slab) { return smem + (slab % G::kStages) * (G::SA + G::SB); };
-  uint8_t* const scales = smem + G::kStages * (G::SA + G::SB);
-  // load d of the wave's LA + LB of slab kt
-  auto load_slab = [&](uint8_t* st, int kt, int d) {
+  constexpr int kLoads = G::LA + G::LB;
+  // load d of the wave's of the loader's slab, into the stage at st
+  auto load = [&](uint8_t* st, int d) {
     if (d < G::LA) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_ptr_t)(st + (wave * G::LA + d) * 1024), 16,
-                                               ga[d & 1] + (d >> 1) * 16 * lda, kt * 128, 0, 0);
+                                               ga[d & 1] + (d >> 1) * 16 * lda, lkt * 128, 0, 0);
     } else {
       const int e = d - G::LA;
-      uint8_t* const to = st + G::SA + (wave * G::LB + e) * 1024;
-      if constexpr (A8)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)to, 16, gb[0] + e * 16 * ldb, kt * 64, 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)to, 16, gb[e & 1] + (e >> 1) * 16 * ldb, kt * 128, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)(st + G::SA + (wave * G::LB + e) * 1024), 16,
+                                               A8 ? gb[0] + e * 16 * ldb : gb[e & 1] + (e >> 1) * 16 * ldb,
+                                               lkt * G::kRowB, 0, 0);
     }
   };
-  auto load_scales = [&](int c) {
-#pragma unroll
-    for (int d = 0; d < G::LS; ++d)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rS, (lds_ptr_t)(scales + (c & 1) * G::kScales + (wave * G::LS + d) * 1024), 16,
-                                               gs + d * 64 * lds_pitch, c * 16, 0, 0);
+  // the loader's next slab, of its next tile past the last (with few slabs to
+  // a tile, the loader is more than one tile ahead)
+  int32_t lat = at;
+  auto advance = [&]() {
+    lkt = __builtin_amdgcn_readfirstlane(lkt + 1);
+    if (lkt == KT) {
+      lkt = 0;
+      lat += tiles.step;
+      slabs_of(place_of<G>(tiles, lat));
+    }
+  };
+  auto load_scales = [&](int c, int buf, int d) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rS, (lds_ptr_t)(scales + buf * G::kScales + (wave * G::LS + d) * 1024), 16,
+                                             gs + d * 64 * pitch, c * 16, 0, 0);
   };
 
-  // fragment reads: lane bases within a stage
-  uint32_t fa[4], fb[4];  // E2M1: piece 2 hs + odd; E4M3: A low / high half, B per half slab
+  // ---- reads: lane bases within a stage, per 16-byte piece (E4M3's B: per half)
+  uint32_t fa[2], fb[2];
   {
     const int ra = wm * 32 * NBM + (lane & 31), rb = wn * 32 * NBN + (lane & 31);
-    const uint32_t a0 = (ra >> 3) * 1024 + (ra & 7) * 64;
-    if constexpr (A8) {
-      const uint32_t b0 = (rb >> 4) * 1024 + (rb & 15) * 64;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        fa[u] = a0 + 16 * ((2 * u + h) ^ row_perm(ra));
-        fb[u] = G::SA + b0 + 16 * ((2 * u + h) ^ row_perm(rb));
-        fa[2 + u] = fb[2 + u] = 0;
-      }
-    } else {
-      const uint32_t b0 = (rb >> 3) * 1024 + (rb & 7) * 64;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        fa[q] = a0 + 512 * h + 16 * (q ^ row_perm(ra));
-        fb[q] = G::SA + b0 + 512 * h + 16 * (q ^ row_perm(rb));
-      }
+    for (int u = 0; u < 2; ++u) {
+      fa[u] = (ra >> 3) * 1024 + (ra & 7) * 64 + 16 * ((2 * u + h) ^ row_perm(ra));
+      fb[u] = G::SA + (A8 ? (rb >> 4) * 1024 + (rb & 15) * 64 : (rb >> 3) * 1024 + (rb & 7) * 64) +
+              16 * ((2 * u + h) ^ row_perm(rb));
     }
   }
-  const uint32_t sa_at = (wm * 32 * NBM + (lane & 31)) * 16 + (A8 ? 0 : 4 * h);
-  const uint32_t sb_at = (G::TM + wn * 32 * NBN + (lane & 31)) * 16 + (A8 ? 0 : 4 * h);
-
+  const uint32_t sa_at = (wm * 32 * NBM + (lane & 31)) * 16, sb_at = (G::TM + wn * 32 * NBN + (lane & 31)) * 16;
   struct Frags {
     typename G::AFrag a[NBM][G::kSteps];
     i32x4 b[NBN][G::kSteps];
@@ -215,248 +376,220 @@ __device__ __forceinline__ void mx_tile(const MxGemmArgs& p, int32_t row0, int32
       }
     } else {
       // A and B blocks in turn, the piece of the half's first MFMAs before the second's
-      const int odd = r / (NBM + NBN), in = r % (NBM + NBN);
-      const int least = NBM < NBN ? NBM : NBN;
-      const bool is_a = in < 2 * least ? (in & 1) == 0 : NBM > NBN;
-      const int blk = in < 2 * least ? in >> 1 : in - least;
-      if (is_a)
-        F.a[blk][odd] = *reinterpret_cast<const i32x4*>(st + fa[2 * hs + odd] + 4096 * blk);
+      static_assert(NBM == NBN || A8, "reads in turn");
+      const int u = r / (NBM + NBN), in = r % (NBM + NBN), blk = in >> 1;
+      if ((in & 1) == 0)
+        F.a[blk][u] = *reinterpret_cast<const i32x4*>(st + fa[u] + 512 * hs + 4096 * blk);
       else
-        F.b[blk][odd] = *reinterpret_cast<const i32x4*>(st + fb[2 * hs + odd] + 4096 * blk);
+        F.b[blk][u] = *reinterpret_cast<const i32x4*>(st + fb[u] + 512 * hs + 4096 * blk);
     }
   };
-  // dword r of slab kt's scales
-  auto read_scale = [&](int kt, int r, int (&S)[NBM + NBN]) {
-    const uint8_t* const at = scales + (kt / G::kPerChunk & 1) * G::kScales + (kt % G::kPerChunk) * (A8 ? 4 : 8);
-    S[r] = *reinterpret_cast<const int*>(at + (r < NBM ? sa_at + 512 * r : sb_at + 512 * (r - NBM)));
+  // slab kt's scales (one dword of E4M3, two of E2M1) of the wave's row block r: A's, then B's
+  i32x2 raw[NBM + NBN];
+  auto read_scales = [&](int kt, int buf, int r) {
+    const uint8_t* const q = scales + buf * G::kScales + (kt % G::kPerChunk) * (A8 ? 4 : 8) +
+                             (r < NBM ? sa_at + 512 * r : sb_at + 512 * (r - NBM));
+    if constexpr (A8)
+      raw[r][0] = *reinterpret_cast<const int*>(q);
+    else
+      raw[r] = *reinterpret_cast<const i32x2*>(q);
+  };
+  // S: the dwords of scales in use, shifted so that bytes 0 and 2 are this
+  // lane's: per half of an E2M1 slab, or (one set) of an E4M3 slab with the
+  // next slab's in the other set.  Each is made from raw during the half
+  // before its use, in the shadow of the MFMAs.
+  int S[2][NBM + NBN];
+  // a scale byte past K may hold anything, also the NaN scale: the bytes of
+  // dword `dword` of slab kt that count
+  auto keep_of = [&](int kt, int dword) -> uint32_t {
+    if (!partial || kt != KT - 1) return ~0u;
+    const int left = p.K - kt * G::kSlabK - 128 * dword;
+    return left >= 128 ? ~0u : left <= 0 ? 0u : (1u << (left / 4)) - 1u;
+  };
+  auto make_scale = [&](int set, int r, int dword, uint32_t keep) {
+    S[set][r] = static_cast<int>((static_cast<uint32_t>(raw[r][dword]) & keep) >> (8 * h));
+  };
+  // The MFMAs are opaque to the compiler's hazard tracking: the wait states
+  // between a VALU write of an operand and its MFMA are given here, behind the
+  // definition of every S that the half uses.
+  auto settle_scales = [&](int set) {
+#pragma unroll
+    for (int r = 0; r < NBM + NBN; ++r) asm volatile("" : "+v"(S[set][r]));
+    asm volatile("s_nop 1" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   f32x16 acc[NBM][NBN];
-#pragma unroll
-  for (int i = 0; i < NBM; ++i)
-#pragma unroll
-    for (int j = 0; j < NBN; ++j) acc[i][j] = f32x16{};
-
-  constexpr int kMfmas = NBM * NBN * G::kSteps;  // per half slab
-  constexpr int kLoads = G::LA + G::LB;
+  constexpr int kBlocks = NBM * NBN, kMfmas = kBlocks * G::kSteps;
   Frags F0, F1;
-  int S[NBM + NBN], Sn[NBM + NBN];
-
-  // Half hs of slab kt on F: its MFMAs, with the reads of the next half slab
-  // into Fn (kRead) and, in the second half, of the next slab's scales, and the
-  // loads of slab kt_load (kLoad) placed behind given MFMAs.
-  auto half_step = [&](auto hs_c, auto read_c, auto load_c, int kt, int kt_load, const Frags& F, Frags& Fn) {
+  // Half hs of a slab on F: its MFMAs, and placed behind given ones the reads
+  // of the next half slab (at st) into Fn; in the first half, LS loads of the
+  // scale chunk c into buffer sbuf (c < 0: none); in the second, the reads of
+  // the next slab's scales and the loads of the loader's slab into `to`; in
+  // the last quarter, the next half's scales from raw (`keep` of them).
+  auto half_step = [&](auto hs_c, const uint8_t* st, uint8_t* to, int kt_next, int buf_next, int c, int sbuf, uint32_t keep,
+                       const Frags& F, Frags& Fn) {
     constexpr int hs = decltype(hs_c)::value;
-    constexpr bool kRead = decltype(read_c)::value, kLoad = decltype(load_c)::value;
-    const uint8_t* const from = stage(hs == 0 ? kt : kt + 1);
-    uint8_t* const to = stage(kt_load);
-    constexpr int kScaleReads = hs == 1 ? NBM + NBN : 0;
-    constexpr int kAllReads = kReads + kScaleReads;
+    constexpr int kSet = A8 ? 0 : hs, kMake = A8 ? 1 : hs ^ 1;
+    constexpr int kAll = kReads + (hs == 1 ? NBM + NBN : 0);
     // reads fill the first half of the MFMAs, loads all of them
-    constexpr int kReadsPer = (kAllReads * 2 + kMfmas - 1) / kMfmas;
-    constexpr int kLoadsPer = (kLoads + kMfmas - 1) / kMfmas;
-    constexpr int kLoadEvery = kMfmas / kLoads > 0 ? kMfmas / kLoads : 1;
+    constexpr int kReadsPer = (kAll * 2 + kMfmas - 1) / kMfmas;
+    constexpr int kLoadsPer = (kLoads + kMfmas - 1) / kMfmas, kLoadEvery = kMfmas / kLoads > 0 ? kMfmas / kLoads : 1;
+    constexpr int kMakeAt = kMfmas * 3 / 4, kMakePer = (NBM + NBN) / (kMfmas - kMakeAt);
+    static_assert(kMakePer * (kMfmas - kMakeAt) == NBM + NBN, "scales in the last quarter");
 #pragma unroll
     for (int m = 0; m < kMfmas; ++m) {
-      const int step = m / (NBM * NBN), i = m / NBN % NBM, j = m % NBN;
-      if constexpr (A8) {
-        mfma<2 * hs>(acc[i][j], F.b[j][0], F.a[i][0], S[NBM + j], S[i]);
-      } else {
-        if (step == 0)
-          mfma<2 * hs>(acc[i][j], F.b[j][0], F.a[i][0], S[NBM + j], S[i]);
-        else
-          mfma<2 * hs + 1>(acc[i][j], F.b[j][G::kSteps - 1], F.a[i][G::kSteps - 1], S[NBM + j], S[i]);
-      }
-      if constexpr (kRead) {
+      const int u = m / kBlocks, i = m / NBN % NBM, j = m % NBN;
+      if constexpr (A8)
+        mfma<2 * hs>(acc[i][j], F.b[j][0], F.a[i][0], S[kSet][NBM + j], S[kSet][i]);
+      else if (u == 0)
+        mfma<0>(acc[i][j], F.b[j][0], F.a[i][0], S[kSet][NBM + j], S[kSet][i]);
+      else
+        mfma<2>(acc[i][j], F.b[j][G::kSteps - 1], F.a[i][G::kSteps - 1], S[kSet][NBM + j], S[kSet][i]);
 #pragma unroll
-        for (int u = 0; u < kReadsPer; ++u) {
-          const int r = m * kReadsPer + u;
-          if (r < kReads)
-            read(from, hs ^ 1, r, Fn);
-          else if (r < kAllReads)
-            read_scale(kt + 1, r - kReads, Sn);
-        }
+      for (int v = 0; v < kReadsPer; ++v) {
+        const int r = m * kReadsPer + v;
+        if (r < kReads)
+          read(st, hs ^ 1, r, Fn);
+        else if (r < kAll)
+          read_scales(kt_next, buf_next, r - kReads);
       }
-      if constexpr (kLoad) {
+      if constexpr (hs == 1) {
         if (m % kLoadEvery == 0) {
 #pragma unroll
-          for (int u = 0; u < kLoadsPer; ++u) {
-            const int d = m / kLoadEvery * kLoadsPer + u;
-            if (d < kLoads) load_slab(to, kt_load, d);
-          }
+          for (int v = 0; v < kLoadsPer; ++v)
+            if (m / kLoadEvery * kLoadsPer + v < kLoads) load(to, m / kLoadEvery * kLoadsPer + v);
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < G::LS; ++d)
+          if (m == kMfmas / 8 + d * kMfmas / G::LS && c >= 0) load_scales(c, sbuf, d);
+      }
+      if constexpr (hs == 1 || !A8) {
+        if (m >= kMakeAt) {
+#pragma unroll
+          for (int v = 0; v < kMakePer; ++v) make_scale(kMake, (m - kMakeAt) * kMakePer + v, hs == 1 ? 0 : 1, keep);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // the scales of the coming slab, from their reads; the MFMAs are opaque to
-  // the compiler's hazard tracking, so the wait states between a VALU write of
-  // an operand and its MFMA are given here
-  auto take_scales = [&]() {
+  // The accumulators to zero, by MFMAs of zeros without a C operand: tied in
+  // place like all their other writes, and half the cycles of 256 VALU writes.
+  auto clear = [&]() {
+    i32x4 zero = {0, 0, 0, 0};
+    asm volatile("" : "+v"(zero));
+    asm volatile("s_nop 3");
 #pragma unroll
-    for (int r = 0; r < NBM + NBN; ++r) {
-      S[r] = A8 ? static_cast<int>(static_cast<uint32_t>(Sn[r]) >> (8 * h)) : Sn[r];
-      asm volatile("" : "+v"(S[r]));
-    }
-    asm volatile("s_nop 3" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < NBM; ++i)
+#pragma unroll
+      for (int j = 0; j < NBN; ++j)
+        asm volatile("v_mfma_f32_32x32x64_f8f6f4 %0, %1, %1, 0 cbsz:4 blgp:4" : "+a"(acc[i][j]) : "v"(zero));
   };
   constexpr std::integral_constant<int, 0> first{};
   constexpr std::integral_constant<int, 1> second{};
-  constexpr std::true_type yes{};
-  constexpr std::false_type no{};
 
-  // prologue: the first stages, chunks 0 and 1 of the scales
-  load_scales(0);
-  if (KC > 1) load_scales(1);
+  // ---- the stream's first stages and its first chunk of scales
+  slabs_of(cur);
+  scales_of(cur);
+#pragma unroll
+  for (int d = 0; d < G::LS; ++d) load_scales(0, 0, d);
 #pragma unroll
   for (int t = 0; t < G::kStages; ++t) {
-    if (t < KT) {
-      if (partial && t == KT - 1) mask_last();
+    mask();
 #pragma unroll
-      for (int d = 0; d < kLoads; ++d) load_slab(stage(t), t, d);
-    }
+    for (int d = 0; d < kLoads; ++d) load(smem + t * G::kStage, d);
+    advance();
   }
-  wait_vmcnt<0>();
+  clear();
+  wait_vmcnt<(G::kStages - 1) * kLoads>();
   barrier_only();
+  uint8_t *s0 = smem, *s1 = smem + G::kStage;  // stages of this slab and the next
 #pragma unroll
-  for (int r = 0; r < kReads; ++r) read(stage(0), 0, r, F0);
+  for (int r = 0; r < kReads; ++r) read(s0, 0, r, F0);
 #pragma unroll
-  for (int r = 0; r < NBM + NBN; ++r) read_scale(0, r, Sn);
+  for (int r = 0; r < NBM + NBN; ++r) read_scales(0, 0, r);
 
-  int kt = 0;
-  for (; kt + G::kStages < KT; ++kt) {
-    wait_lgkmcnt0();
-    take_scales();
-    half_step(first, yes, no, kt, 0, F0, F1);
-    wait_lgkmcnt0();
-    // slab kt + 1 has landed; E4M3: slab kt + 2 may still be on its way
-    wait_vmcnt<(G::kStages - 2) * kLoads>();
-    barrier_only();
-    // this slab's stage is free, and so is its chunk's buffer after its last slab
-    if (kt % G::kPerChunk == G::kPerChunk - 1 && kt / G::kPerChunk + 2 < KC) load_scales(kt / G::kPerChunk + 2);
-    if (partial && kt + G::kStages == KT - 1) mask_last();
-    half_step(second, yes, yes, kt, kt + G::kStages, F1, F0);
-  }
-  for (; kt + 1 < KT; ++kt) {  // nothing left to load
-    wait_lgkmcnt0();
-    take_scales();
-    half_step(first, yes, no, kt, 0, F0, F1);
-    wait_lgkmcnt0();
-    wait_vmcnt<0>();
-    barrier_only();
-    half_step(second, yes, no, kt, 0, F1, F0);
-  }
-  wait_lgkmcnt0();
-  take_scales();
-  half_step(first, yes, no, kt, 0, F0, F1);
-  wait_lgkmcnt0();
-  half_step(second, no, no, kt, 0, F1, F0);
-  // the last MFMAs' result latency, then every accumulator redefined behind it
-  asm volatile("s_nop 7\n s_nop 7\n s_nop 7\n s_nop 7" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < NBM; ++i)
-#pragma unroll
-    for (int j = 0; j < NBN; ++j) asm volatile("" : "+a"(acc[i][j]));
+  for (int r = 0; r < NBM + NBN; ++r) make_scale(A8 ? 1 : 0, r, 0, keep_of(0, 0));
 
-  // Epilogue.  A lane holds, of block (i, j), row l % 32 and columns 8 (r / 4)
-  // + 4 h + r % 4.  A whole bf16 wave block without C goes through LDS, so
-  // that a row is stored in 16-byte pieces; else four columns at a time.
-  constexpr int WM = 32 * NBM, WN = 32 * NBN;
-  const int32_t wrow = wm * WM, wcol = wn * WN;
-  const int64_t bias0 = b_row0 + n0 + wcol;  // p.bias: N values per group, as B's rows
-  int elane = lane;  // the epilogue's addresses are not hoisted above the loop
-  asm volatile("" : "+v"(elane));
-  const int el = elane & 31, eh = elane >> 5;
-  if constexpr (kBf16) {
-    constexpr int kPitch = WN * 2 + 16;  // padded: rows start on different banks
-    static_assert(4 * WM * kPitch <= G::kLds, "epilogue LDS");
-    const bool whole = rows - wrow >= WM && cols - wcol >= WN && p.beta == 0.0f &&
-                       ((reinterpret_cast<uint64_t>(p.D) | (static_cast<uint64_t>(p.ldd) * 2)) & 15) == 0;
-    barrier_only();  // every wave is past its reads of the stages
-    if (whole) {
-      uint8_t* const w = smem + wave * WM * kPitch;
+  int buf = 0, kv = 0;   // buffer of the current chunk of scales; slab of the current tile
+  bool behind = false;   // kStores stores were issued since the last loads of a slab
+  for (;;) {
+    const int kt = __builtin_amdgcn_readfirstlane(kv);
+    const bool last = kt + 1 == KT;
+    const int kt_next = last ? 0 : kt + 1;
+    // the chunk of scales after this one, loaded at its first slab: what its
+    // buffer held was used up before the last barrier
+    int c = -1;
+    if (kt % G::kPerChunk == 0) {
+      c = kt / G::kPerChunk + 1;
+      if (c == KC) {
+        c = 0;
+        scales_of(next);
+      }
+    }
+    // what the barrier waits for: the next slab has landed, and so has the next
+    // chunk of scales if it is read now.  Operations retire in order, and behind
+    // the next slab's loads are those of the slabs after it, a tile's stores
+    // and the scales' loads.
+    const int wait = last && kt % G::kPerChunk == 0 ? 2 : kt == 0 && behind ? 1 : 0;
+    wait_lgkmcnt0();
+    if constexpr (A8) {
+#pragma unroll
+      for (int r = 0; r < NBM + NBN; ++r) S[0][r] = S[1][r];
+    }
+    settle_scales(0);
+    half_step(first, s0, nullptr, 0, 0, c, buf ^ 1, A8 ? 0u : keep_of(kt, 1), F0, F1);
+    wait_lgkmcnt0();
+    if constexpr (!A8) settle_scales(1);
+    if (wait == 0)
+      wait_vmcnt<(G::kStages - 2) * kLoads>();
+    else if (wait == 1)
+      wait_vmcnt<(G::kStages - 2) * kLoads + G::kStores + G::LS>();
+    else
+      wait_vmcnt<0>();
+    barrier_only();
+    if (kt_next % G::kPerChunk == 0) buf ^= 1;
+    mask();
+    half_step(second, s1, s0, kt_next, buf, -1, 0, keep_of(kt_next, 0), F1, F0);
+    advance();
+    s0 = s1;
+    s1 = s1 + G::kStage == scales ? smem : s1 + G::kStage;
+    kv = kt_next;
+    if (last) {
+      // the last MFMAs' result latency, then every accumulator redefined behind it
+      asm volatile("s_nop 7\n s_nop 7\n s_nop 7\n s_nop 7" ::: "memory");
 #pragma unroll
       for (int i = 0; i < NBM; ++i)
 #pragma unroll
-        for (int j = 0; j < NBN; ++j)
+        for (int j = 0; j < NBN; ++j) asm volatile("" : "+a"(acc[i][j]));
+      int elane = lane;  // the epilogue's addresses are not hoisted above the loop
+      asm volatile("" : "+v"(elane));
+      behind = store_block_of<kBf16, NBM, NBN>(fresh_args(), cur, wm, wn, elane, acc);
+      if (next.rows == 0) return;
+      clear();
+      at += tiles.step;
+      cur = next;
+      next = place_of<G>(tiles, at + tiles.step);
+      // the next tile's first fragments once more: kept in registers over the
+      // epilogue they would push others out to memory, and every slab's waits
+      // would then include those
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int c = 32 * j + 8 * g + 4 * eh;
-            float v[4];
+      for (int r = 0; r < kReads; ++r) read(s0, 0, r, F0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[e] = p.alpha * acc[i][j][4 * g + e];
-              if (p.bias) v[e] += load_value<true>(p.bias, bias0 + c + e);
-            }
-            *reinterpret_cast<u32x2*>(w + (32 * i + el) * kPitch + 2 * c) =
-                u32x2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
-          }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own area: no barrier
-      constexpr int kLanes = WN / 8, kRowsPer = 64 / kLanes;  // lanes per row, rows per instruction
-      const int er = elane / kLanes, ec = elane % kLanes;
-      uint16_t* const d = static_cast<uint16_t*>(p.D) + static_cast<int64_t>(row0 + wrow + er) * p.ldd + n0 + wcol + 8 * ec;
+      for (int r = 0; r < NBM + NBN; ++r) read_scales(0, buf, r);
 #pragma unroll
-      for (int t = 0; t < WM / kRowsPer; ++t)
-        *reinterpret_cast<u32x4*>(d + static_cast<int64_t>(t * kRowsPer) * p.ldd) =
-            *reinterpret_cast<const u32x4*>(w + (t * kRowsPer + er) * kPitch + 16 * ec);
-      return;
+      for (int r = 0; r < NBM + NBN; ++r) make_scale(A8 ? 1 : 0, r, 0, keep_of(0, 0));
     }
   }
-  const bool wide = wide_rows<kBf16>(p);
-#pragma unroll
-  for (int i = 0; i < NBM; ++i) {
-    const int32_t r = wrow + 32 * i + el;
-    if (r >= rows) continue;
-#pragma unroll
-    for (int j = 0; j < NBN; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int32_t c = wcol + 32 * j + 8 * g + 4 * eh;
-        if (c < cols)
-          store_four<kBf16>(p, b_row0, row0 + r, n0 + c, cols - c, wide,
-                            f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]});
-      }
-  }
-}
-
-// Height, in tiles, of a band of tile rows that is walked column by column.
-constexpr int kBand = 4;
-
-// Place w of the order of a tiles_m x tiles_n grid.
-__device__ __forceinline__ void order_tile(int32_t w, int32_t tiles_m, int32_t tiles_n, int32_t& tm, int32_t& tn) {
-  const int32_t band = w / (kBand * tiles_n), first = band * kBand;
-  const int32_t high = min(kBand, tiles_m - first), in = w - band * kBand * tiles_n;
-  tm = first + in % high;
-  tn = in / high;
 }
 
 template <bool A8, bool kBf16, int NBM, int NBN>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NBM* NBN == 16 ? 1 : 2, NBM* NBN == 16 ? 1 : 2)))
 void mx_gemm_tile_kernel(MxGemmArgs p) {
-  using G = Geo<A8, NBM, NBN>;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[G::kLds];
-  const int32_t tiles_n = (p.N + G::TN - 1) / G::TN;
-  const int32_t row_tiles = p.offsets ? count_group_tiles(p.offsets, p.groups, p.M, G::TM) : (p.M + G::TM - 1) / G::TM;
-  // workgroup b runs on XCD b mod 8: each XCD takes one contiguous range of the tile order
-  const int32_t T = row_tiles * tiles_n, x = static_cast<int32_t>(blockIdx.x) % kXcds, i = static_cast<int32_t>(blockIdx.x) / kXcds;
-  const int32_t each = T / kXcds, more = T % kXcds;
-  if (i >= each + (x < more ? 1 : 0)) return;
-  const int32_t t = x * each + min(x, more) + i;
-  int32_t tm, tn, row0 = 0, rows = p.M;
-  int64_t b_row0 = 0;
-  if (p.offsets) {
-    const GroupTile g = find_group_tile(p.offsets, p.groups, p.M, G::TM, t / tiles_n);
-    if (g.group < 0) return;
-    // the group's tiles are a grid of their own, from its first row tile on
-    row0 = g.row0 - g.index * G::TM;
-    rows = g.rows + g.index * G::TM;
-    b_row0 = static_cast<int64_t>(g.group) * p.N;
-    order_tile(t - (t / tiles_n - g.index) * tiles_n, g.tiles, tiles_n, tm, tn);
-  } else {
-    order_tile(t, row_tiles, tiles_n, tm, tn);
-  }
-  mx_tile<A8, kBf16, NBM, NBN>(p, row0 + tm * G::TM, rows - tm * G::TM, tn * G::TN, b_row0, smem);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Geo<A8, NBM, NBN>::kLds];
+  run_tiles<A8, kBf16, NBM, NBN>(p, smem);
 }
 
 template <bool A8, bool kBf16, int NBM, int NBN>
@@ -465,8 +598,9 @@ static hipError_t tile_t(const MxGemmArgs& a, hipStream_t st) {
   const int64_t row_tiles = a.offsets ? most_group_tiles(a.M, a.groups, G::TM) : (a.M + G::TM - 1) / G::TM;
   const int64_t T = row_tiles * ((a.N + G::TN - 1) / G::TN);
   if (T > INT32_MAX / 2) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_gemm_tile_kernel<A8, kBf16, NBM, NBN>), dim3(static_cast<unsigned>((T + kXcds - 1) / kXcds * kXcds)),
-                     dim3(256), 0, st, a);
+  const int64_t most = static_cast<int64_t>(a.cus) * G::kWgs;
+  const int64_t grid = ((T < most ? T : most) + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL((mx_gemm_tile_kernel<A8, kBf16, NBM, NBN>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

@@ -9,6 +9,12 @@ namespace mx {
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 
+// A pointer into global memory, said so in its type: where it was read from
+// memory, the compiler cannot know, and flat accesses (which also occupy the
+// LDS counter) would be the result.
+template <typename T>
+using global_ptr = __attribute__((address_space(1))) T*;
+
 constexpr uint32_t kOutOfRange = 0x80000000u;  // an offset past every descriptor's end: the load gives zeros
 
 // Buffer descriptor of a wave-uniform base and byte count (below 2^31).
@@ -39,41 +45,55 @@ struct GroupTile {
 // take 64 groups at a time: a scan of their tile counts, then a ballot.
 // Every lane of the wave calls it with the same arguments.  total: all tiles.
 __device__ __forceinline__ int32_t group_bound(const int32_t* offsets, int32_t i, int32_t M) {
-  return min(max(offsets[i], 0), M);
+  return min(max(((global_ptr<const int32_t>)offsets)[i], 0), M);
+}
+
+// 64 groups, one per lane: their rows lo .. hi - 1 and the tiles of the
+// groups up to and including the lane's.
+struct GroupLanes {
+  int32_t lo, hi, incl;
+};
+__device__ __forceinline__ GroupLanes load_groups(const int32_t* offsets, int32_t groups, int32_t M, int32_t tm,
+                                                  int32_t base = 0) {
+  const int lane = threadIdx.x & 63;
+  GroupLanes g{0, 0, 0};
+  if (base + lane < groups) {
+    g.lo = group_bound(offsets, base + lane, M);
+    g.hi = max(g.lo, group_bound(offsets, base + lane + 1, M));
+  }
+  g.incl = (g.hi - g.lo + tm - 1) / tm;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const int32_t v = __shfl_up(g.incl, s);
+    if (lane >= s) g.incl += v;
+  }
+  return g;
+}
+
+// Row tile u among these 64 groups, `before` tiles and `base` groups before them.
+__device__ __forceinline__ GroupTile group_tile_of(const GroupLanes& g, int32_t base, int32_t before, int32_t tm,
+                                                   int32_t u) {
+  const uint64_t past = __ballot(before + g.incl > u);
+  if (past == 0) return GroupTile{-1, 0, 0, 0, 0};
+  const int first = __builtin_ctzll(past);
+  const int32_t lo = __builtin_amdgcn_readlane(g.lo, first), hi = __builtin_amdgcn_readlane(g.hi, first);
+  GroupTile t;
+  t.group = base + first;
+  t.tiles = (hi - lo + tm - 1) / tm;
+  t.index = u - (before + __builtin_amdgcn_readlane(g.incl, first) - t.tiles);
+  t.row0 = lo + t.index * tm;
+  t.rows = hi - t.row0;
+  return t;
 }
 
 __device__ __forceinline__ GroupTile find_group_tile(const int32_t* offsets, int32_t groups, int32_t M, int32_t tm,
                                                      int32_t u) {
-  const int lane = threadIdx.x & 63;
   int32_t before = 0;  // tiles of the groups already passed
   for (int32_t base = 0; base < groups; base += 64) {
-    const int32_t g = base + lane;
-    int32_t lo = 0, hi = 0;
-    if (g < groups) {
-      lo = group_bound(offsets, g, M);
-      hi = max(lo, group_bound(offsets, g + 1, M));
-    }
-    const int32_t n = (hi - lo + tm - 1) / tm;
-    int32_t incl = n;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int32_t v = __shfl_up(incl, s);
-      if (lane >= s) incl += v;
-    }
-    const uint64_t past = __ballot(before + incl > u);
-    if (past != 0) {
-      const int first = __builtin_ctzll(past);
-      GroupTile t;
-      const int32_t n1 = __builtin_amdgcn_readlane(n, first), i1 = __builtin_amdgcn_readlane(incl, first);
-      const int32_t lo1 = __builtin_amdgcn_readlane(lo, first), hi1 = __builtin_amdgcn_readlane(hi, first);
-      t.group = base + first;
-      t.tiles = n1;
-      t.index = u - (before + i1 - n1);
-      t.row0 = lo1 + t.index * tm;
-      t.rows = hi1 - t.row0;
-      return t;
-    }
-    before += __builtin_amdgcn_readlane(incl, 63);
+    const GroupLanes g = load_groups(offsets, groups, M, tm, base);
+    const GroupTile t = group_tile_of(g, base, before, tm, u);
+    if (t.group >= 0) return t;
+    before += __builtin_amdgcn_readlane(g.incl, 63);
   }
   return GroupTile{-1, 0, 0, 0, 0};
 }
@@ -100,9 +120,9 @@ inline int64_t most_group_tiles(int64_t M, int64_t groups, int64_t tm) {
 template <bool kBf16>
 __device__ __forceinline__ float load_value(const void* p, int64_t i) {
   if constexpr (kBf16)
-    return __builtin_bit_cast(float, static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+    return __builtin_bit_cast(float, static_cast<uint32_t>(((global_ptr<const uint16_t>)p)[i]) << 16);
   else
-    return static_cast<const float*>(p)[i];
+    return ((global_ptr<const float>)p)[i];
 }
 
 // Four neighbouring values of row `row` from column `col`: alpha * v + beta *
@@ -122,18 +142,18 @@ __device__ __forceinline__ void store_four(const MxGemmArgs& a, int64_t bias0, i
   }
   const int64_t at = row * a.ldd + col;
   if constexpr (kBf16) {
-    uint16_t* d = static_cast<uint16_t*>(a.D) + at;
+    const auto d = (global_ptr<uint16_t>)a.D + at;
     if (wide && n >= 4) {
-      *reinterpret_cast<u32x2*>(d) = u32x2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
+      *(global_ptr<u32x2>)d = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (e < n) d[e] = static_cast<uint16_t>(bf16_rne(v[e]));
+        if (e < n) d[e] = static_cast<uint16_t>(pack_bf16(v[e], 0.0f));
     }
   } else {
-    float* d = static_cast<float*>(a.D) + at;
+    const auto d = (global_ptr<float>)a.D + at;
     if (wide && n >= 4) {
-      *reinterpret_cast<f32x4*>(d) = v;
+      *(global_ptr<f32x4>)d = v;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)

@@ -108,6 +108,8 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
       uint8_t* y = static_cast<uint8_t*>(a.y) + row * a.ldy + 8 * i;
       if constexpr (kAligned) {
         *reinterpret_cast<u32x2*>(y) = q;
+      } else if (n >= 8) {
+        *reinterpret_cast<u32x2_any*>(y) = q;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)

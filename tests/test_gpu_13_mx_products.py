@@ -158,6 +158,79 @@ def test_nan_blocks_reach_their_rows_and_columns_alone(M, N, K, a_format):
     assert np.array_equal(nan, want)
 
 
+@pytest.mark.parametrize("M,N,K", [(4, 40, 544), (70, 100, 96), (600, 520, 1120)])
+@pytest.mark.parametrize("a_format", ["E2M1", "E4M3"])
+def test_scale_bytes_past_k_are_not_used(M, N, K, a_format):
+    import torch
+    A, As, a = make(M, K, a_format, 5)
+    B, Bs, b = make(N, K, "E2M1", 6)
+    D, E = torch.empty((M, N), device="cuda"), torch.empty((M, N), device="cuda")
+    with dg.MxPlan(M, N, K, a_format=a_format, out_dtype="F32") as p:
+        p.run(up(A), up(As), up(B), up(Bs), D)
+        As[:, K // 32:], Bs[:, K // 32:] = 255, 255
+        p.run(up(A), up(As), up(B), up(Bs), E)
+    assert torch.equal(D, E)
+
+
+def random_codes(rows, cols, fmt, seed):
+    """Random codes and scales of an MX tensor on the GPU, and its values (fp64)."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = torch.randint(0, 256, (rows, cols // 2 if fmt == "E2M1" else cols), generator=g, device="cuda", dtype=torch.uint8)
+    if fmt == "E4M3":
+        codes = codes & 0xB7                 # no NaN, nothing above 2
+    scales = torch.randint(120, 130, (rows, mx.scale_pitch(cols)), generator=g, device="cuda", dtype=torch.uint8)
+    table = torch.from_numpy(mx.e2m1_to_f64(np.arange(16)) if fmt == "E2M1" else codecs.e4m3_to_f64(np.arange(256))).cuda()
+    c = torch.stack((codes & 15, codes >> 4), -1).reshape(rows, cols) if fmt == "E2M1" else codes
+    v = table[c.long()] * torch.exp2(scales[:, :cols // 32].double() - 127).repeat_interleave(32, -1)
+    return codes, scales, v
+
+
+def check_on_gpu(D, a, b, out):
+    """check() for large products, on the GPU: same bar."""
+    ref = a @ b.T
+    size = a.norm(dim=1)[:, None] * b.norm(dim=1)[None]
+    diff = (D.double() - ref).abs()
+    assert bool((diff <= (2.0 ** -8 if out == "BF16" else 2.0 ** -24) * ref.abs() + parity.TIGHT_ACCUM["e4m3"] * size).all())
+
+
+# more tiles than workgroups, so that each walks several: 256 x 256 and 128 x 128 tiles, one slab of K and more,
+# whole and partial ones
+@pytest.mark.parametrize("K", [32, 96, 160, 256, 288, 544, 1024, 1184])
+@pytest.mark.parametrize("M,N,out", [(5900, 5000, "BF16"), (5888, 5120, "BF16"), (5900, 5000, "F32"), (2500, 4700, "BF16")])
+@pytest.mark.parametrize("a_format", ["E2M1", "E4M3"])
+def test_many_tiles(M, N, K, a_format, out):
+    import torch
+    log("many tiles", M, N, K, a_format, out)
+    A, As, a = random_codes(M, K, a_format, 1)
+    B, Bs, b = random_codes(N, K, "E2M1", 2)
+    D = torch.full((M, N), 7.0, dtype=torch_out(out), device="cuda")
+    with dg.MxPlan(M, N, K, a_format=a_format, out_dtype=out) as p:
+        p.run(A, As, B, Bs, D)
+    check_on_gpu(D, a, b, out)
+
+
+@pytest.mark.parametrize("E", [5, 100])
+@pytest.mark.parametrize("a_format", ["E2M1", "E4M3"])
+@pytest.mark.parametrize("K", [96, 544])
+def test_many_grouped_tiles(E, K, a_format):
+    import torch
+    g = np.random.default_rng(E)
+    counts = g.multinomial(9000, g.dirichlet(np.full(E, 0.7)))
+    counts[E // 2] = 0
+    M, N = int(counts.sum()) + 3, 3400
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    log("many grouped tiles", E, K, a_format, M)
+    A, As, a = random_codes(M, K, a_format, 1)
+    B, Bs, b = random_codes(E * N, K, "E2M1", 2)
+    D = torch.full((M, N), -5.0, dtype=torch.bfloat16, device="cuda")
+    with dg.MxPlan(M, N, K, groups=E, a_format=a_format) as p:
+        p.run(A, As, B, Bs, D, offsets=up(off))
+    for e in range(E):
+        check_on_gpu(D[off[e]:off[e + 1]], a[off[e]:off[e + 1]], b[e * N:(e + 1) * N], "BF16")
+    assert bool((D[off[-1]:] == -5.0).all())
+
+
 def test_fewer_rows_than_the_plan():
     for rows in (1, 40, 200, 600):
         dense(600, 512, 512, "E4M3", "BF16", rows=rows)
