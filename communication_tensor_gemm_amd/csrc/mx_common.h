@@ -236,20 +236,23 @@ struct Raw8<PT_F32> {
   }
 };
 
-// The e4m3 conversion instruction gives NaN past 464: clamp first, which
-// keeps a NaN only if asked (v_med3 would turn it into a bound).
-__device__ __forceinline__ float clamp448(float v) {
-  return v != v ? v : __builtin_amdgcn_fmed3f(v, -448.0f, 448.0f);
-}
-
-// Eight values to e4m3 bytes, round to nearest even, saturating; NaN stays NaN.
+// Eight values to e4m3 bytes, round to nearest even.  The conversion
+// instruction gives NaN past 464, so the values are clamped to +-448 first;
+// v_med3 makes a bound of a NaN, so where there can be one it is kept apart.
+template <bool kNan>
 __device__ __forceinline__ u32x2 pack_e4m3(const float (&v)[8]) {
+  float c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c[j] = __builtin_amdgcn_fmed3f(v[j], -448.0f, 448.0f);
+    if constexpr (kNan) c[j] = v[j] != v[j] ? v[j] : c[j];
+  }
   u32x2 r;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     int w = 0;
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(v[4 * h]), clamp448(v[4 * h + 1]), w, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(v[4 * h + 2]), clamp448(v[4 * h + 3]), w, true);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * h], c[4 * h + 1], w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * h + 2], c[4 * h + 3], w, true);
     r[h] = static_cast<uint32_t>(w);
   }
   return r;
@@ -284,31 +287,97 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float& inv) 
   return static_cast<uint32_t>(b);
 }
 
-// Largest magnitude of four lanes' eight values each (a block of 32), as bits.
-__device__ __forceinline__ uint32_t block_amax(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
-  // lanes 4b .. 4b + 3 hold one block: exchange within the quad
+// The larger of a block's four lanes' values: the lanes 4b .. 4b + 3 of one
+// block exchange within the quad.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
   m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xB1, 0xf, 0xf, true)));
-  m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4E, 0xf, 0xf, true)));
-  return m;
+  return max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4E, 0xf, 0xf, true)));
 }
 
-// Store one lane's eight elements of a block (every lane of the quad calls it).
+// Store one lane's eight codes of a block, and the block's scale byte.
+template <int FMT>
+__device__ __forceinline__ void store_codes(u32x2 w, uint32_t byte, uint8_t* codes, int64_t code_row, int col8,
+                                            uint8_t* scales, int64_t scale_row) {
+  // a block without a scale has zero codes
+  w[0] = byte == 255u ? 0u : w[0];
+  if constexpr (FMT == MX_E4M3) {
+    w[1] = byte == 255u ? 0u : w[1];
+    *reinterpret_cast<u32x2*>(codes + code_row + 8 * static_cast<int64_t>(col8)) = w;
+  } else {
+    *reinterpret_cast<uint32_t*>(codes + code_row + 4 * static_cast<int64_t>(col8)) = w[0];
+  }
+  if ((col8 & 3) == 0) scales[scale_row + (col8 >> 2)] = static_cast<uint8_t>(byte);
+}
+
+// Quantise and store one lane's eight elements of a block (every lane of the
+// quad calls it).
 template <int FMT>
 __device__ __forceinline__ void store_block(const float (&v)[8], uint8_t* codes, int64_t code_row, int col8,
                                             uint8_t* scales, int64_t scale_row) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
   float inv;
-  const uint32_t byte = block_scale<FMT>(block_amax(v), inv);
+  const uint32_t byte = block_scale<FMT>(quad_max(m), inv);
   float q[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = byte == 255u ? 0.0f : v[j] * inv;
+  for (int j = 0; j < 8; ++j) q[j] = v[j] * inv;
+  u32x2 w{0, 0};
   if constexpr (FMT == MX_E4M3)
-    *reinterpret_cast<u32x2*>(codes + code_row + 8 * static_cast<int64_t>(col8)) = pack_e4m3(q);
+    w = pack_e4m3<false>(q);
   else
-    *reinterpret_cast<uint32_t*>(codes + code_row + 4 * static_cast<int64_t>(col8)) = pack_e2m1(q);
-  if ((col8 & 3) == 0) scales[scale_row + (col8 >> 2)] = static_cast<uint8_t>(byte);
+    w[0] = pack_e2m1(q);
+  store_codes<FMT>(w, byte, codes, code_row, col8, scales, scale_row);
+}
+
+// The same from eight bf16 values as they were loaded, on pairs: the
+// magnitudes' maximum and the clamp to 448 * 2^X are 16-bit integer
+// operations, and the conversions take bf16 pairs and the scale (4 against 11
+// instructions per element; they, not memory, bounded the quantiser).
+template <int FMT>
+__device__ __forceinline__ void store_block_bf16(u32x4 v, uint8_t* codes, int64_t code_row, int col8, uint8_t* scales,
+                                                 int64_t scale_row) {
+  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+  uint32_t mag[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mag[j] = v[j] & 0x7fff7fffu;
+  auto max2 = [](uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+  };
+  const uint32_t m2 = max2(max2(mag[0], mag[1]), max2(mag[2], mag[3]));
+  float inv;
+  const uint32_t byte = block_scale<FMT>(quad_max(max(m2 << 16, m2 & 0xffff0000u)), inv);
+  // 2^X; the conversion takes its exponent field, so 0 stands for 2^-127
+  const float scale = __builtin_bit_cast(float, byte << 23);
+  u32x2 w{0, 0};
+  if constexpr (FMT == MX_E4M3) {
+    const uint32_t top = ((byte + 8u) << 7 | 0x60u) * 0x10001u;  // 448 * 2^X
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t t = __builtin_bit_cast(
+          uint32_t, __builtin_elementwise_min(__builtin_bit_cast(u16x2, mag[j]), __builtin_bit_cast(u16x2, top)));
+      c[j] = t | (v[j] & 0x80008000u);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s16x2 r{0, 0};
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, c[2 * h]), scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, c[2 * h + 1]), scale, true);
+      w[h] = __builtin_bit_cast(uint32_t, r);
+    }
+  } else {
+    // (a bit cast of a vector's element would take the vector's first)
+    const uint32_t e0 = v[0], e1 = v[1], e2 = v[2], e3 = v[3];
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, e0), scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, e1), scale, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, e2), scale, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, e3), scale, 3);
+    w[0] = r;
+  }
+  store_codes<FMT>(w, byte, codes, code_row, col8, scales, scale_row);
 }
 
 }  // namespace mx

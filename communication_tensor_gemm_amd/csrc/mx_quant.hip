@@ -14,56 +14,58 @@ namespace mx {
 constexpr int kThreads = 256, kPieces = 4;
 constexpr int kSegment = kThreads * kPieces;  // eight-element pieces of one workgroup
 
-// A workgroup's pieces: a segment of one row, or several short rows.
-struct Pieces {
-  int64_t row0;
-  int32_t rows, d, first, n;  // rows, pieces per row, first piece of the row, pieces in all
+// Pieces are numbered through all rows (d to a row), a workgroup takes
+// kSegment of them, so every lane has work whatever the row's length.  n / d
+// for n below 2^31 is one product and a shift: with 2^(s-1) < d <= 2^s and m =
+// floor(2^(31+s) / d) + 1, it is floor(n m / 2^(31+s)).
+struct Rows {
+  uint32_t d, m, shift;  // shift = s - 1
+  uint32_t pieces;       // of a chunk of rows (one per blockIdx.y), below 2^31
+  int64_t rows;          // of a chunk
 };
-__device__ __forceinline__ Pieces my_pieces(int64_t rows, int32_t d, int32_t per_group, int32_t segment) {
-  Pieces p;
-  p.d = d;
-  p.row0 = static_cast<int64_t>(blockIdx.x) * per_group;
-  const int64_t left = rows - p.row0;
-  p.rows = static_cast<int32_t>(left < per_group ? left : per_group);
-  p.first = static_cast<int32_t>(blockIdx.y) * segment;
-  p.n = per_group == 1 ? min(segment, d - p.first) : p.rows * d;
-  return p;
-}
+__device__ __forceinline__ uint32_t row_of(const Rows& r, uint32_t n) { return __umulhi(n, r.m) >> r.shift; }
 
 template <int T, int FMT, bool kAligned>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a, int32_t per_group, int32_t segment) {
-  const int32_t d = static_cast<int32_t>(a.cols / 8);
+__global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a, Rows rows) {
   const int64_t pitch = scale_pitch(a.cols), row_bytes = mx_row_bytes(a.cols, FMT);
-  const Pieces p = my_pieces(a.rows, d, per_group, segment);
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * rows.rows;
+  const int64_t left = (a.rows - row0) * rows.d;
+  const uint32_t pieces = left < rows.pieces ? static_cast<uint32_t>(left) : rows.pieces;
+  const uint32_t first = blockIdx.x * kSegment + threadIdx.x;
   Raw8<T> raw[kPieces];
   int64_t row[kPieces];
   int32_t col[kPieces];
 #pragma unroll
   for (int c = 0; c < kPieces; ++c) {
-    const int32_t i = c * kThreads + static_cast<int32_t>(threadIdx.x);
-    if (i < p.n) {
-      const int32_t r = per_group == 1 ? 0 : i / d;
-      row[c] = p.row0 + r;
-      col[c] = p.first + (i - r * d);
+    const uint32_t i = first + c * kThreads;
+    if (i < pieces) {
+      const uint32_t r = row_of(rows, i);
+      row[c] = row0 + r;
+      col[c] = static_cast<int32_t>(i - r * rows.d);
       raw[c].template load<kAligned>(a.x, row[c] * a.ldx + 8 * static_cast<int64_t>(col[c]), 8);
     }
   }
 #pragma unroll
   for (int c = 0; c < kPieces; ++c) {
     // the pieces of a block are four adjacent lanes: all of them are in or none is
-    if (c * kThreads + static_cast<int32_t>(threadIdx.x) < p.n) {
-      float v[8];
-      raw[c].get(v);
-      store_block<FMT>(v, a.codes, row[c] * row_bytes, col[c], a.scales, row[c] * pitch);
+    if (first + c * kThreads < pieces) {
+      if constexpr (T == PT_BF16) {
+        store_block_bf16<FMT>(raw[c].w, a.codes, row[c] * row_bytes, col[c], a.scales, row[c] * pitch);
+      } else {
+        float v[8];
+        raw[c].get(v);
+        store_block<FMT>(v, a.codes, row[c] * row_bytes, col[c], a.scales, row[c] * pitch);
+      }
     }
   }
-  // the row's scale bytes past K / 32
-  const int32_t pad = static_cast<int32_t>(pitch - a.cols / kMxBlock);
-  if (pad > 0 && p.first + segment >= d)
-    for (int32_t i = threadIdx.x; i < p.rows * pad; i += kThreads) {
-      const int32_t r = i / pad;
-      a.scales[(p.row0 + r) * pitch + a.cols / kMxBlock + (i - r * pad)] = 0;
-    }
+  // the scale bytes past K / 32, by the lane of the row's last block
+  const int32_t blocks = static_cast<int32_t>(a.cols / kMxBlock), pad = static_cast<int32_t>(pitch) - blocks;
+  if (pad > 0) {
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c)
+      if (first + c * kThreads < pieces && col[c] == 4 * blocks - 4)
+        for (int32_t k = 0; k < pad; ++k) a.scales[row[c] * pitch + blocks + k] = 0;
+  }
 }
 
 // bytes of one E8M0 scale as a float (255: NaN)
@@ -73,21 +75,23 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
 }
 
 template <int T, int FMT, bool kAligned>
-__global__ __launch_bounds__(kThreads) void dequantize_kernel(DequantizeArgs a, int32_t per_group, int32_t segment) {
-  const int32_t d = static_cast<int32_t>(a.cols / 8);
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(DequantizeArgs a, Rows rows) {
   const int64_t pitch = scale_pitch(a.cols), row_bytes = mx_row_bytes(a.cols, FMT);
-  const Pieces p = my_pieces(a.rows, d, per_group, segment);
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * rows.rows;
+  const int64_t left = (a.rows - row0) * rows.d;
+  const uint32_t pieces = left < rows.pieces ? static_cast<uint32_t>(left) : rows.pieces;
+  const uint32_t first = blockIdx.x * kSegment + threadIdx.x;
   u32x2 w[kPieces];
   uint32_t sb[kPieces];
   int64_t row[kPieces];
   int32_t col[kPieces];
 #pragma unroll
   for (int c = 0; c < kPieces; ++c) {
-    const int32_t i = c * kThreads + static_cast<int32_t>(threadIdx.x);
-    if (i < p.n) {
-      const int32_t r = per_group == 1 ? 0 : i / d;
-      row[c] = p.row0 + r;
-      col[c] = p.first + (i - r * d);
+    const uint32_t i = first + c * kThreads;
+    if (i < pieces) {
+      const uint32_t r = row_of(rows, i);
+      row[c] = row0 + r;
+      col[c] = static_cast<int32_t>(i - r * rows.d);
       if constexpr (FMT == MX_E4M3)
         w[c] = *reinterpret_cast<const u32x2*>(a.codes + row[c] * row_bytes + 8 * static_cast<int64_t>(col[c]));
       else
@@ -97,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(DequantizeArgs a, 
   }
 #pragma unroll
   for (int c = 0; c < kPieces; ++c) {
-    if (c * kThreads + static_cast<int32_t>(threadIdx.x) >= p.n) continue;
+    if (first + c * kThreads >= pieces) continue;
     float v[8];
     if constexpr (FMT == MX_E4M3) {
 #pragma unroll
@@ -123,46 +127,41 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(DequantizeArgs a, 
   }
 }
 
-// rows per workgroup (short rows) and pieces per segment (long rows)
-static void split_rows(int64_t rows, int64_t cols, int32_t* per_group, int32_t* segment, dim3* grid) {
-  const int64_t d = cols / 8;
-  int64_t segs = 1;
-  if (d >= kSegment) {
-    *per_group = 1;
-    segs = (d + kSegment - 1) / kSegment;
-    // equal segments of whole blocks
-    *segment = static_cast<int32_t>(((d + segs - 1) / segs + 3) / 4 * 4);
-    segs = (d + *segment - 1) / *segment;
-  } else {
-    *per_group = static_cast<int32_t>(kSegment / d);
-    *segment = static_cast<int32_t>(d);
-  }
-  *grid = dim3(static_cast<unsigned>((rows + *per_group - 1) / *per_group), static_cast<unsigned>(segs));
+static Rows split_rows(int64_t rows, int64_t cols, dim3* grid) {
+  Rows r;
+  r.d = static_cast<uint32_t>(cols / 8);
+  uint32_t s = 0;
+  while ((uint64_t{1} << s) < r.d) ++s;
+  r.shift = s - 1;  // d is at least 4
+  r.m = static_cast<uint32_t>((uint64_t{1} << (31 + s)) / r.d + 1);
+  const int64_t most = ((int64_t{1} << 31) - kSegment) / r.d;  // rows whose pieces stay below 2^31
+  r.rows = rows < most ? rows : most;
+  r.pieces = static_cast<uint32_t>(r.rows * r.d);
+  *grid = dim3((r.pieces + kSegment - 1) / kSegment, static_cast<unsigned>((rows + r.rows - 1) / r.rows));
+  return r;
 }
 
 template <int T, int FMT>
 static hipError_t quantize_t(const QuantizeArgs& a, hipStream_t st) {
-  int32_t per_group, segment;
   dim3 grid;
-  split_rows(a.rows, a.cols, &per_group, &segment, &grid);
+  const Rows rows = split_rows(a.rows, a.cols, &grid);
   const int es = T == PT_F32 ? 4 : 2;
   if (((reinterpret_cast<uint64_t>(a.x) | static_cast<uint64_t>(a.ldx * es)) & 15) == 0)
-    hipLaunchKernelGGL((quantize_kernel<T, FMT, true>), grid, dim3(kThreads), 0, st, a, per_group, segment);
+    hipLaunchKernelGGL((quantize_kernel<T, FMT, true>), grid, dim3(kThreads), 0, st, a, rows);
   else
-    hipLaunchKernelGGL((quantize_kernel<T, FMT, false>), grid, dim3(kThreads), 0, st, a, per_group, segment);
+    hipLaunchKernelGGL((quantize_kernel<T, FMT, false>), grid, dim3(kThreads), 0, st, a, rows);
   return hipGetLastError();
 }
 
 template <int T, int FMT>
 static hipError_t dequantize_t(const DequantizeArgs& a, hipStream_t st) {
-  int32_t per_group, segment;
   dim3 grid;
-  split_rows(a.rows, a.cols, &per_group, &segment, &grid);
+  const Rows rows = split_rows(a.rows, a.cols, &grid);
   const int es = T == PT_F32 ? 4 : 2;
   if (((reinterpret_cast<uint64_t>(a.y) | static_cast<uint64_t>(a.ldy * es)) & 15) == 0)
-    hipLaunchKernelGGL((dequantize_kernel<T, FMT, true>), grid, dim3(kThreads), 0, st, a, per_group, segment);
+    hipLaunchKernelGGL((dequantize_kernel<T, FMT, true>), grid, dim3(kThreads), 0, st, a, rows);
   else
-    hipLaunchKernelGGL((dequantize_kernel<T, FMT, false>), grid, dim3(kThreads), 0, st, a, per_group, segment);
+    hipLaunchKernelGGL((dequantize_kernel<T, FMT, false>), grid, dim3(kThreads), 0, st, a, rows);
   return hipGetLastError();
 }
 

@@ -72,6 +72,14 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
       }
     }
   }
+  // the weight is on its way while the row is summed
+  Raw8<T> wr[V];
+#pragma unroll
+  for (int c = 0; c < V; ++c) {
+    const int i = c * span + t;
+    wr[c].zero();
+    if (i < d) wr[c].template load<kAligned>(a.weight, 8 * i, a.cols - 8 * i);
+  }
   float ss = 0.0f;
 #pragma unroll
   for (int c = 0; c < V; ++c) {
@@ -91,11 +99,9 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
     const int i = c * span + t;
     if (i >= d) continue;
     const int n = a.cols - 8 * i;
-    Raw8<T> wr;
-    wr.template load<kAligned>(a.weight, 8 * i, n);
     float f[8], w[8];
     x[c].get(f);
-    wr.get(w);
+    wr[c].get(w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
     if constexpr (OUT == NO_SAME) {
@@ -104,7 +110,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
     } else if constexpr (OUT == NO_E4M3) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= a.inv_scale;
-      const u32x2 q = pack_e4m3(f);
+      const u32x2 q = pack_e4m3<true>(f);
       uint8_t* y = static_cast<uint8_t*>(a.y) + row * a.ldy + 8 * i;
       if constexpr (kAligned) {
         *reinterpret_cast<u32x2*>(y) = q;
@@ -180,10 +186,11 @@ static hipError_t norm_out(int out, const NormArgs& a, hipStream_t st) {
 // registers (the row's lanes hold the same columns every time), and writes
 // it out once as a row of `partial`; a second kernel adds those rows.  No
 // atomics: the order of every sum is fixed, so the result is the same bit
-// for bit from run to run.  With one piece per lane (rows of up to 8192
-// columns) the next row's loads are in flight while the current row's sum
-// crosses the waves; longer rows have no registers for that, and above 16384
-// columns the row itself is read again (from the L2) after its sum.
+// for bit from run to run.  With one piece per lane (of bf16, one or two; rows
+// of up to 8192 and 16384 columns) the next row's loads are in flight while
+// the current row's sum crosses the waves; longer rows have no registers for
+// that, and above 16384 columns the row itself is read again (from the L2)
+// after its sum.
 template <int T, int V, bool kAligned>
 __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArgs a, int W) {
   __shared__ float red[2][kMaxWaves];
@@ -192,7 +199,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArg
   const int d = (a.cols + 7) / 8;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const float inv_n = 1.0f / static_cast<float>(a.cols);
-  constexpr bool kAhead = V == 1, kHold = V <= 2;
+  constexpr bool kAhead = V == 1 || (V == 2 && T == PT_BF16), kHold = V <= 2;
   constexpr int H = kHold ? V : 1, N = kAhead ? V : 1;
   float dw[V][8];
 #pragma unroll
@@ -225,16 +232,20 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArg
   auto scale = [&](int64_t r) { return r < a.rows ? a.rstd[r] : 0.0f; };
   if constexpr (kAhead) {
     s1 = scale(row);
-    fetch(row, 0, dy1[0], h1[0], dh1[0]);
+#pragma unroll
+    for (int c = 0; c < V; ++c) fetch(row, c, dy1[c], h1[c], dh1[c]);
   }
   for (int64_t k = 0; k < turns; ++k) {
     if constexpr (kAhead) {
       s = s1;
-      dy[0] = dy1[0];
-      h[0] = h1[0];
-      dh[0] = dh1[0];
       s1 = scale(row + step);
-      fetch(row + step, 0, dy1[0], h1[0], dh1[0]);
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        dy[c] = dy1[c];
+        h[c] = h1[c];
+        dh[c] = dh1[c];
+        fetch(row + step, c, dy1[c], h1[c], dh1[c]);
+      }
     } else {
       s = scale(row);
       if constexpr (kHold) {
@@ -242,45 +253,49 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArg
         for (int c = 0; c < V; ++c) fetch(row, c, dy[c], h[c], dh[c]);
       }
     }
-    float dot = 0.0f;
+    // With y = dy and x = h: the row's sum is s * sum(y w x), a column's share
+    // of dw is (y s) x, and dx = s (y w) + dh - x s^3 mean(y w x).
+    float dot = 0.0f, yw[kHold ? V : 1][8], xs[kHold ? V : 1][8];
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       const int q = kHold ? c : 0;
       if constexpr (!kHold) __builtin_amdgcn_sched_barrier(0);  // one piece in registers at a time
       if constexpr (!kHold) fetch(row, c, dy[0], h[0], dh[0]);
       if constexpr (V > 1) weight(c * span + t);
-      float y[8], x[8], w[8];
+      float y[8], w[8];
       dy[q].get(y);
-      h[q].get(x);
+      h[q].get(xs[q]);
       wr.get(w);
       float d8 = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float n = x[j] * s;
-        d8 = __builtin_fmaf(y[j] * w[j], n, d8);
-        dw[c][j] = __builtin_fmaf(y[j], n, dw[c][j]);
+        yw[q][j] = y[j] * w[j];
+        d8 = __builtin_fmaf(yw[q][j], xs[q][j], d8);
+        dw[c][j] = __builtin_fmaf(y[j] * s, xs[q][j], dw[c][j]);
       }
       dot += d8;
     }
     // two sets of slots: a wave may be one turn ahead of another's reads
-    const float mean = row_sum(dot, red[k & 1], W) * inv_n;
+    const float k3 = -(s * s * s) * (row_sum(dot, red[k & 1], W) * inv_n);
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       const int i = c * span + t, q = kHold ? c : 0;
-      if constexpr (!kHold) __builtin_amdgcn_sched_barrier(0);
-      if constexpr (!kHold) fetch(row, c, dy[0], h[0], dh[0]);
-      if constexpr (V > 1) weight(i);
+      if constexpr (!kHold) {
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(row, c, dy[0], h[0], dh[0]);
+        weight(i);
+        float y[8], w[8];
+        dy[0].get(y);
+        h[0].get(xs[0]);
+        wr.get(w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) yw[0][j] = y[j] * w[j];
+      }
       if (row >= a.rows || i >= d) continue;
-      float y[8], x[8], w[8], e[8], o[8];
-      dy[q].get(y);
-      h[q].get(x);
-      wr.get(w);
+      float e[8], o[8];
       dh[q].get(e);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = x[j] * s;
-        o[j] = __builtin_fmaf(__builtin_fmaf(-n, mean, y[j] * w[j]), s, e[j]);
-      }
+      for (int j = 0; j < 8; ++j) o[j] = __builtin_fmaf(xs[q][j], k3, __builtin_fmaf(yw[q][j], s, e[j]));
       Raw8<T> out;
       out.set(o);
       out.template store<kAligned>(a.dx, row * a.lddx + 8 * i, a.cols - 8 * i);
@@ -307,12 +322,13 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArg
     return;
   }
 #pragma unroll
-  for (int c = 0; c < V; ++c)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = 8 * (c * span + t) + j;
-      if (col < a.cols) a.partial[static_cast<int64_t>(blockIdx.x) * a.cols + col] = dw[c][j];
-    }
+  for (int c = 0; c < V; ++c) {
+    const int i = c * span + t;
+    if (i >= d) continue;
+    Raw8<PT_F32> out;
+    out.set(dw[c]);
+    out.template store<false>(a.partial, static_cast<int64_t>(blockIdx.x) * a.cols + 8 * i, a.cols - 8 * i);
+  }
 }
 
 // Adds the rows of `partial`: 64 columns per workgroup, 16 waves over the rows.
@@ -323,6 +339,7 @@ __global__ __launch_bounds__(1024) void rms_norm_dweight_kernel(const float* par
   const int col = static_cast<int>(blockIdx.x) * 64 + lane;
   float v = 0.0f;
   if (col < cols)
+#pragma unroll 8
     for (int b = wave; b < blocks; b += 16) v += partial[static_cast<int64_t>(b) * cols + col];
   sums[wave][lane] = v;
   __syncthreads();
@@ -335,15 +352,17 @@ __global__ __launch_bounds__(1024) void rms_norm_dweight_kernel(const float* par
 }
 
 // One row per workgroup of W waves, or four rows of one wave each where a row
-// has at most 512 columns.
-static void backward_shape(int64_t rows, int64_t cols, int* W, int* groups, int64_t* blocks) {
-  const int d = static_cast<int>((cols + 7) / 8);
+// has at most 512 columns.  bf16 rows take two pieces to a lane, so that two
+// workgroups of half the threads share a CU and one moves data while the
+// other's sum crosses its waves; fp32 has the registers for one.  As many
+// workgroups as the chip holds at a time.
+static void backward_shape(int type, int64_t rows, int64_t cols, int* W, int* groups, int64_t* blocks) {
+  const int d = static_cast<int>((cols + 7) / 8), pieces = type == PT_BF16 && d > 64 ? 2 : 1;
   *W = 1;
-  while (*W < kMaxWaves && 64 * *W < d) *W *= 2;
+  while (*W < kMaxWaves && 64 * *W * pieces < d) *W *= 2;
   *groups = cols <= 512 ? 4 : 1;
-  const int64_t most = 8192 / (64 * *W * *groups);  // 2 workgroups of 1024 threads per CU, 8 of fewer
-  const int64_t want = (rows + *groups - 1) / *groups;
-  const int64_t cap = 256 * (most < 2 ? 2 : (most > 4 ? 4 : most));
+  const int waves = *W * *groups, fit = waves >= 16 ? 1 : (waves >= 8 ? 2 : 4);
+  const int64_t want = (rows + *groups - 1) / *groups, cap = 256 * fit;
   *blocks = want < cap ? want : cap;
 }
 
@@ -366,7 +385,7 @@ static hipError_t backward_t(const NormBackwardArgs& a, hipStream_t st) {
   const bool aligned = (m & 15) == 0 && a.cols % 8 == 0;
   int W, groups;
   int64_t blocks;
-  backward_shape(a.rows, a.cols, &W, &groups, &blocks);
+  backward_shape(T, a.rows, a.cols, &W, &groups, &blocks);
   const int d = (a.cols + 7) / 8, v = (d + 64 * W - 1) / (64 * W);
   if (blocks == 0)
     ;  // no rows: the second kernel writes zeros
@@ -392,9 +411,10 @@ hipError_t launch_rms_norm(int type, int out, const NormArgs& a, hipStream_t st)
 
 int64_t rms_norm_backward_blocks(int64_t rows, int64_t cols) {
   int W, groups;
-  int64_t blocks;
-  mx::backward_shape(rows, cols, &W, &groups, &blocks);
-  return blocks;
+  int64_t f32, bf16;
+  mx::backward_shape(PT_F32, rows, cols, &W, &groups, &f32);
+  mx::backward_shape(PT_BF16, rows, cols, &W, &groups, &bf16);
+  return f32 > bf16 ? f32 : bf16;
 }
 
 hipError_t launch_rms_norm_backward(int type, const NormBackwardArgs& a, hipStream_t st) {
