@@ -59,63 +59,77 @@ def _raise(rc: int, plan=None):
     raise DistGemmError(rc, msg.decode() if msg else "")
 
 
+_raw_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream_of(stream, device: int) -> Optional[int]:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device) or None
+        return _raw_stream(device) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
 
 
+# A call of a few microseconds is mostly these checks and the launch: each is
+# one comparison where the argument is right, and the message is made where not.
+
 def _device(t, name) -> int:
     """The device of an operator's first tensor, which has to be the current one."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
     d = t.get_device()
-    if d != torch._C._cuda_getDevice():
+    if d < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if d != _current():
         raise ValueError(f"{name} is on GPU {d}, which is not the current device")
     return d
 
 
-def _rows(t, name, dtype, rows, cols, device) -> int:
+def _rows(t, name, dtype, shape, device) -> int:
     """Checks a matrix whose rows are contiguous; its leading dimension."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, is {t.dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on GPU {device}")
-    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
-        raise ValueError(f"{name} must be {rows} x {cols}, is {tuple(t.shape)}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _wrong(t, name, (dtype,), tuple(shape), device)
     s0, s1 = t.stride()
+    rows, cols = shape
     if s1 != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    if rows <= 1:
-        return max(s0, cols)
     if s0 < cols:
-        raise ValueError(f"the rows of {name} overlap")
+        if rows > 1:
+            raise ValueError(f"the rows of {name} overlap")
+        return cols
     return s0
 
 
 def _flat(t, name, dtypes, count, device):
     """Checks a tensor of `count` elements without gaps."""
+    if t.dtype not in dtypes or t.numel() != count or not t.is_contiguous() or t.get_device() != device:
+        _wrong(t, name, dtypes, count, device)
+
+
+def _wrong(t, name, dtypes, size, device):
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, is {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on GPU {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.numel() != count:
-        raise ValueError(f"{name} must have {count} elements, has {t.numel()}")
+    if isinstance(size, tuple):
+        raise ValueError(f"{name} must be {' x '.join(map(str, size))}, is {tuple(t.shape)}")
+    if t.numel() != size:
+        raise ValueError(f"{name} must have {size} elements, has {t.numel()}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _elem(t, name) -> int:
+def _matrix(t, name):
+    """(device, element type, shape) of an operator's first tensor."""
+    d = _device(t, name)
     e = _ELEM_OF.get(t.dtype)
     if e is None:
         raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, is {t.dtype}")
-    return e
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return d, e, shape
 
 
 def _format(f) -> int:
-    v = _enum(MX_FORMATS, f) if not isinstance(f, str) else MX_FORMATS.get(f, -1)
+    v = MX_FORMATS.get(f, f)
     if v not in (0, 1):
         raise ValueError(f"unknown MX format {f!r}")
     return v
@@ -133,11 +147,10 @@ def _mx_pair(codes, scales, fmt, rows, cols, device, name=""):
 
 def dist_gemm_mx_quantize(x, format, codes, scales, stream=None):
     """Quantise x (rows x cols, f32 or bf16, rows at any pitch) to the MX tensor (codes, scales)."""
-    d, e, fmt = _device(x, "x"), _elem(x, "x"), _format(format)
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix")
-    rows, cols = x.size(0), x.size(1)
-    ld = _rows(x, "x", x.dtype, rows, cols, d)
+    d, e, shape = _matrix(x, "x")
+    fmt = _format(format)
+    rows, cols = shape
+    ld = _rows(x, "x", x.dtype, shape, d)
     _mx_pair(codes, scales, fmt, rows, cols, d)
     rc = lib.dist_gemm_mx_quantize(x.data_ptr(), ld, e, rows, cols, fmt, codes.data_ptr(), scales.data_ptr(),
                                    _stream_of(stream, d))
@@ -147,11 +160,10 @@ def dist_gemm_mx_quantize(x, format, codes, scales, stream=None):
 
 def dist_gemm_mx_dequantize(codes, scales, format, y, stream=None):
     """The values of the MX tensor (codes, scales) into y (rows x cols, f32 or bf16, rows at any pitch)."""
-    d, e, fmt = _device(y, "y"), _elem(y, "y"), _format(format)
-    if y.dim() != 2:
-        raise ValueError("y must be a matrix")
-    rows, cols = y.size(0), y.size(1)
-    ld = _rows(y, "y", y.dtype, rows, cols, d)
+    d, e, shape = _matrix(y, "y")
+    fmt = _format(format)
+    rows, cols = shape
+    ld = _rows(y, "y", y.dtype, shape, d)
     _mx_pair(codes, scales, fmt, rows, cols, d)
     rc = lib.dist_gemm_mx_dequantize(codes.data_ptr(), scales.data_ptr(), fmt, rows, cols, y.data_ptr(), ld, e,
                                      _stream_of(stream, d))
@@ -166,37 +178,37 @@ def dist_gemm_rms_norm(x, weight, y, eps=1e-6, output="SAME", residual=None, h=N
     output: "SAME" (y of x's type), "E4M3" (y holds e4m3 of the result over
     `scale`, the operand of an E4M3 plan with that scale), "MX_E4M3" or
     "MX_E2M1" (y the codes and `scales` the scales of an MX tensor)."""
-    d, e = _device(x, "x"), _elem(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix")
+    d, e, shape = _matrix(x, "x")
     out = NORM_OUTPUTS.get(output, -1)
-    if out < 0:
-        raise ValueError(f"unknown output {output!r}")
-    t, rows, cols = x.dtype, x.size(0), x.size(1)
-    ldx = _rows(x, "x", t, rows, cols, d)
+    t = x.dtype
+    rows, cols = shape
+    ldx = _rows(x, "x", t, shape, d)
     _flat(weight, "weight", (t,), cols, d)
-    if (residual is None) != (h is None):
+    ldr = ldh = ldy = 0
+    pr = ph = ps = pt = None
+    if residual is not None and h is not None:
+        ldr, ldh = _rows(residual, "residual", t, shape, d), _rows(h, "h", t, shape, d)
+        pr, ph = residual.data_ptr(), h.data_ptr()
+    elif residual is not None or h is not None:
         raise ValueError("residual and h go together")
-    ldr = ldh = 0
-    if residual is not None:
-        ldr, ldh = _rows(residual, "residual", t, rows, cols, d), _rows(h, "h", t, rows, cols, d)
     if rstd is not None:
         _flat(rstd, "rstd", (torch.float32,), rows, d)
-    ldy = 0
+        pt = rstd.data_ptr()
     if out == 0:
-        ldy = _rows(y, "y", t, rows, cols, d)
+        ldy = _rows(y, "y", t, shape, d)
     elif out == 1:
         if y.dtype not in _BYTES:
-            raise ValueError(f"y must be torch.float8_e4m3fn or torch.uint8, is {y.dtype}")
-        ldy = _rows(y, "y", y.dtype, rows, cols, d)
-    else:
+            _wrong(y, "y", _BYTES, tuple(shape), d)
+        ldy = _rows(y, "y", y.dtype, shape, d)
+    elif out > 1:
         if scales is None:
             raise ValueError("an MX output needs scales")
         _mx_pair(y, scales, out - 2, rows, cols, d)
-    rc = lib.dist_gemm_rms_norm(x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
-                                weight.data_ptr(), e, rows, cols, eps, out, scale, y.data_ptr(), ldy,
-                                None if scales is None else scales.data_ptr(), None if h is None else h.data_ptr(),
-                                ldh, None if rstd is None else rstd.data_ptr(), _stream_of(stream, d))
+        ps = scales.data_ptr()
+    else:
+        raise ValueError(f"unknown output {output!r}")
+    rc = lib.dist_gemm_rms_norm(x.data_ptr(), ldx, pr, ldr, weight.data_ptr(), e, rows, cols, eps, out, scale,
+                                y.data_ptr(), ldy, ps, ph, ldh, pt, _stream_of(stream, d))
     if rc:
         _raise(rc)
 
@@ -208,12 +220,11 @@ def dist_gemm_rms_norm_workspace(rows: int, cols: int) -> int:
 
 def dist_gemm_rms_norm_backward(dy, h, rstd, weight, dx, dweight, workspace, dh=None, stream=None):
     """Gradient of dist_gemm_rms_norm: dx (+ dh, the residual stream's own gradient) and dweight (fp32)."""
-    d, e = _device(h, "h"), _elem(h, "h")
-    if h.dim() != 2:
-        raise ValueError("h must be a matrix")
-    t, rows, cols = h.dtype, h.size(0), h.size(1)
-    ldh, lddy, lddx = (_rows(m, n, t, rows, cols, d) for m, n in ((h, "h"), (dy, "dy"), (dx, "dx")))
-    lddh = 0 if dh is None else _rows(dh, "dh", t, rows, cols, d)
+    d, e, shape = _matrix(h, "h")
+    t = h.dtype
+    rows, cols = shape
+    ldh, lddy, lddx = _rows(h, "h", t, shape, d), _rows(dy, "dy", t, shape, d), _rows(dx, "dx", t, shape, d)
+    lddh = 0 if dh is None else _rows(dh, "dh", t, shape, d)
     _flat(weight, "weight", (t,), cols, d)
     _flat(rstd, "rstd", (torch.float32,), rows, d)
     _flat(dweight, "dweight", (torch.float32,), cols, d)
@@ -255,15 +266,18 @@ class MxPlan:
         if self.handle is None:
             raise ValueError("the plan is closed")
         d, N = self.device, self.N
-        rows = D.size(0)
-        ldd = _rows(D, "D", self._dtype, rows, N, d)
+        shape = D.shape
+        rows = shape[0]
+        if len(shape) != 2 or shape[1] != N:
+            raise ValueError(f"D must be rows x {N}, is {tuple(shape)}")
+        ldd = _rows(D, "D", self._dtype, shape, d)
         _flat(A, "A", _BYTES if self.a_format else (torch.uint8,), rows * self._ka, d)
         _flat(A_scales, "A_scales", _SCALES, rows * self._pitch, d)
         _flat(B, "B", (torch.uint8,), self._nb, d)
         _flat(B_scales, "B_scales", _SCALES, self._ns, d)
         ldc, pc, pb, po = 0, None, None, None
         if C is not None:
-            ldc, pc = _rows(C, "C", self._dtype, rows, N, d), C.data_ptr()
+            ldc, pc = _rows(C, "C", self._dtype, shape, d), C.data_ptr()
         if bias is not None:
             _flat(bias, "bias", (self._dtype,), max(self.groups, 1) * N, d)
             pb = bias.data_ptr()

@@ -102,6 +102,8 @@ hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t st);
 // on tiles of `size` (256 or 128) squared
 hipError_t launch_mx_gemm_tile(int size, const MxGemmArgs& a, hipStream_t st);
 
+// Bytes of the last-level cache, shared by the whole device.
+constexpr int64_t kLastLevelCache = int64_t{256} << 20;
 // Largest row that the RMS norm kernels keep in registers.
 constexpr int kNormMaxCols = 32768;
 
@@ -129,21 +131,44 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
-// Eight consecutive elements of a row, as loaded.  Not kAligned: addresses
-// are aligned to the element only, and a piece may have n < 8 elements left
-// in its row (those past the end read as zero); whole pieces still move in
-// accesses of full width (a 1021 x 5123 fp32 norm, whose rows start on every
-// 4-byte offset: 31 us with element accesses, 14 us with these).
+// How a kernel reaches its large matrices.  ANY: addresses are aligned to the
+// element only, and a piece of eight may have fewer left in its row; whole
+// pieces still move in accesses of full width (a 1021 x 5123 fp32 norm, whose
+// rows start on every 4-byte offset: 31 us with element accesses, 10 with
+// these).  ALIGNED: 16-byte aligned, whole pieces.  STREAM: the same, past
+// the caches: where the operator's bytes exceed the last-level cache, what it
+// writes could not stay there (quantise 8192 x 13312: 59 us without, 54 with;
+// norm 8192 x 16384: 165 and 156; its gradient 8192 x 8192: 107 and 99), and
+// below that size the next operator finds it there.
+enum Access { ANY = 0, ALIGNED = 1, STREAM = 2 };
+
+template <int A, typename V>
+__device__ __forceinline__ V load_wide(const V* p) {
+  if constexpr (A == STREAM)
+    return __builtin_nontemporal_load(p);
+  else
+    return *p;
+}
+template <int A, typename V>
+__device__ __forceinline__ void store_wide(V* p, V v) {
+  if constexpr (A == STREAM)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
+// Eight consecutive elements of a row, as loaded.  n (ANY): elements left in
+// the row from the first; those past its end read as zero.
 template <int T>
 struct Raw8;
 template <>
 struct Raw8<PT_BF16> {
   u32x4 w;
-  template <bool kAligned>
+  template <int A>
   __device__ __forceinline__ void load(const void* p, int64_t i, int n) {
     const uint16_t* s = static_cast<const uint16_t*>(p) + i;
-    if constexpr (kAligned) {
-      w = *reinterpret_cast<const u32x4*>(s);
+    if constexpr (A != ANY) {
+      w = load_wide<A>(reinterpret_cast<const u32x4*>(s));
     } else if (n >= 8) {
       w = *reinterpret_cast<const u32x4_any*>(s);
     } else {
@@ -168,11 +193,11 @@ struct Raw8<PT_BF16> {
     for (int j = 0; j < 4; ++j) w[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
     get(f);
   }
-  template <bool kAligned>
+  template <int A>
   __device__ __forceinline__ void store(void* p, int64_t i, int n) const {
     uint16_t* d = static_cast<uint16_t*>(p) + i;
-    if constexpr (kAligned) {
-      *reinterpret_cast<u32x4*>(d) = w;
+    if constexpr (A != ANY) {
+      store_wide<A>(reinterpret_cast<u32x4*>(d), w);
     } else if (n >= 8) {
       *reinterpret_cast<u32x4_any*>(d) = w;
     } else {
@@ -185,12 +210,12 @@ struct Raw8<PT_BF16> {
 template <>
 struct Raw8<PT_F32> {
   f32x4 a, b;
-  template <bool kAligned>
+  template <int A>
   __device__ __forceinline__ void load(const void* p, int64_t i, int n) {
     const float* s = static_cast<const float*>(p) + i;
-    if constexpr (kAligned) {
-      a = *reinterpret_cast<const f32x4*>(s);
-      b = *reinterpret_cast<const f32x4*>(s + 4);
+    if constexpr (A != ANY) {
+      a = load_wide<A>(reinterpret_cast<const f32x4*>(s));
+      b = load_wide<A>(reinterpret_cast<const f32x4*>(s + 4));
     } else if (n >= 8) {
       a = *reinterpret_cast<const f32x4_any*>(s);
       b = *reinterpret_cast<const f32x4_any*>(s + 4);
@@ -217,12 +242,12 @@ struct Raw8<PT_F32> {
       b[j] = f[j + 4];
     }
   }
-  template <bool kAligned>
+  template <int A>
   __device__ __forceinline__ void store(void* p, int64_t i, int n) const {
     float* d = static_cast<float*>(p) + i;
-    if constexpr (kAligned) {
-      *reinterpret_cast<f32x4*>(d) = a;
-      *reinterpret_cast<f32x4*>(d + 4) = b;
+    if constexpr (A != ANY) {
+      store_wide<A>(reinterpret_cast<f32x4*>(d), a);
+      store_wide<A>(reinterpret_cast<f32x4*>(d + 4), b);
     } else if (n >= 8) {
       *reinterpret_cast<f32x4_any*>(d) = a;
       *reinterpret_cast<f32x4_any*>(d + 4) = b;
@@ -295,23 +320,24 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
 }
 
 // Store one lane's eight codes of a block, and the block's scale byte.
-template <int FMT>
+template <int FMT, int A>
 __device__ __forceinline__ void store_codes(u32x2 w, uint32_t byte, uint8_t* codes, int64_t code_row, int col8,
                                             uint8_t* scales, int64_t scale_row) {
   // a block without a scale has zero codes
   w[0] = byte == 255u ? 0u : w[0];
   if constexpr (FMT == MX_E4M3) {
     w[1] = byte == 255u ? 0u : w[1];
-    *reinterpret_cast<u32x2*>(codes + code_row + 8 * static_cast<int64_t>(col8)) = w;
+    store_wide<A>(reinterpret_cast<u32x2*>(codes + code_row + 8 * static_cast<int64_t>(col8)), w);
   } else {
-    *reinterpret_cast<uint32_t*>(codes + code_row + 4 * static_cast<int64_t>(col8)) = w[0];
+    const uint32_t lo = w[0];
+    store_wide<A>(reinterpret_cast<uint32_t*>(codes + code_row + 4 * static_cast<int64_t>(col8)), lo);
   }
   if ((col8 & 3) == 0) scales[scale_row + (col8 >> 2)] = static_cast<uint8_t>(byte);
 }
 
 // Quantise and store one lane's eight elements of a block (every lane of the
 // quad calls it).
-template <int FMT>
+template <int FMT, int A>
 __device__ __forceinline__ void store_block(const float (&v)[8], uint8_t* codes, int64_t code_row, int col8,
                                             uint8_t* scales, int64_t scale_row) {
   uint32_t m = 0;
@@ -327,14 +353,14 @@ __device__ __forceinline__ void store_block(const float (&v)[8], uint8_t* codes,
     w = pack_e4m3<false>(q);
   else
     w[0] = pack_e2m1(q);
-  store_codes<FMT>(w, byte, codes, code_row, col8, scales, scale_row);
+  store_codes<FMT, A>(w, byte, codes, code_row, col8, scales, scale_row);
 }
 
 // The same from eight bf16 values as they were loaded, on pairs: the
 // magnitudes' maximum and the clamp to 448 * 2^X are 16-bit integer
 // operations, and the conversions take bf16 pairs and the scale (4 against 11
 // instructions per element; they, not memory, bounded the quantiser).
-template <int FMT>
+template <int FMT, int A>
 __device__ __forceinline__ void store_block_bf16(u32x4 v, uint8_t* codes, int64_t code_row, int col8, uint8_t* scales,
                                                  int64_t scale_row) {
   typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
@@ -377,7 +403,7 @@ __device__ __forceinline__ void store_block_bf16(u32x4 v, uint8_t* codes, int64_
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, e3), scale, 3);
     w[0] = r;
   }
-  store_codes<FMT>(w, byte, codes, code_row, col8, scales, scale_row);
+  store_codes<FMT, A>(w, byte, codes, code_row, col8, scales, scale_row);
 }
 
 }  // namespace mx

@@ -25,7 +25,7 @@ struct Rows {
 };
 __device__ __forceinline__ uint32_t row_of(const Rows& r, uint32_t n) { return __umulhi(n, r.m) >> r.shift; }
 
-template <int T, int FMT, bool kAligned>
+template <int T, int FMT, int A>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a, Rows rows) {
   const int64_t pitch = scale_pitch(a.cols), row_bytes = mx_row_bytes(a.cols, FMT);
   const int64_t row0 = static_cast<int64_t>(blockIdx.y) * rows.rows;
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a, Rows
       const uint32_t r = row_of(rows, i);
       row[c] = row0 + r;
       col[c] = static_cast<int32_t>(i - r * rows.d);
-      raw[c].template load<kAligned>(a.x, row[c] * a.ldx + 8 * static_cast<int64_t>(col[c]), 8);
+      raw[c].template load<A>(a.x, row[c] * a.ldx + 8 * static_cast<int64_t>(col[c]), 8);
     }
   }
 #pragma unroll
@@ -50,11 +50,11 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a, Rows
     // the pieces of a block are four adjacent lanes: all of them are in or none is
     if (first + c * kThreads < pieces) {
       if constexpr (T == PT_BF16) {
-        store_block_bf16<FMT>(raw[c].w, a.codes, row[c] * row_bytes, col[c], a.scales, row[c] * pitch);
+        store_block_bf16<FMT, A>(raw[c].w, a.codes, row[c] * row_bytes, col[c], a.scales, row[c] * pitch);
       } else {
         float v[8];
         raw[c].get(v);
-        store_block<FMT>(v, a.codes, row[c] * row_bytes, col[c], a.scales, row[c] * pitch);
+        store_block<FMT, A>(v, a.codes, row[c] * row_bytes, col[c], a.scales, row[c] * pitch);
       }
     }
   }
@@ -74,7 +74,7 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
   return __builtin_bit_cast(float, b == 0u ? 0x00400000u : b << 23);
 }
 
-template <int T, int FMT, bool kAligned>
+template <int T, int FMT, int A>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(DequantizeArgs a, Rows rows) {
   const int64_t pitch = scale_pitch(a.cols), row_bytes = mx_row_bytes(a.cols, FMT);
   const int64_t row0 = static_cast<int64_t>(blockIdx.y) * rows.rows;
@@ -93,9 +93,9 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(DequantizeArgs a, 
       row[c] = row0 + r;
       col[c] = static_cast<int32_t>(i - r * rows.d);
       if constexpr (FMT == MX_E4M3)
-        w[c] = *reinterpret_cast<const u32x2*>(a.codes + row[c] * row_bytes + 8 * static_cast<int64_t>(col[c]));
+        w[c] = load_wide<A>(reinterpret_cast<const u32x2*>(a.codes + row[c] * row_bytes + 8 * static_cast<int64_t>(col[c])));
       else
-        w[c][0] = *reinterpret_cast<const uint32_t*>(a.codes + row[c] * row_bytes + 4 * static_cast<int64_t>(col[c]));
+        w[c][0] = load_wide<A>(reinterpret_cast<const uint32_t*>(a.codes + row[c] * row_bytes + 4 * static_cast<int64_t>(col[c])));
       sb[c] = a.scales[row[c] * pitch + (col[c] >> 2)];
     }
   }
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(DequantizeArgs a, 
     for (int j = 0; j < 8; ++j) v[j] *= s;
     Raw8<T> out;
     out.set(v);
-    out.template store<kAligned>(a.y, row[c] * a.ldy + 8 * static_cast<int64_t>(col[c]), 8);
+    out.template store<A>(a.y, row[c] * a.ldy + 8 * static_cast<int64_t>(col[c]), 8);
   }
 }
 
@@ -146,10 +146,12 @@ static hipError_t quantize_t(const QuantizeArgs& a, hipStream_t st) {
   dim3 grid;
   const Rows rows = split_rows(a.rows, a.cols, &grid);
   const int es = T == PT_F32 ? 4 : 2;
-  if (((reinterpret_cast<uint64_t>(a.x) | static_cast<uint64_t>(a.ldx * es)) & 15) == 0)
-    hipLaunchKernelGGL((quantize_kernel<T, FMT, true>), grid, dim3(kThreads), 0, st, a, rows);
+  if (((reinterpret_cast<uint64_t>(a.x) | static_cast<uint64_t>(a.ldx * es)) & 15) != 0)
+    hipLaunchKernelGGL((quantize_kernel<T, FMT, ANY>), grid, dim3(kThreads), 0, st, a, rows);
+  else if (a.rows * a.cols * (es + (FMT == MX_E4M3)) < kLastLevelCache)
+    hipLaunchKernelGGL((quantize_kernel<T, FMT, ALIGNED>), grid, dim3(kThreads), 0, st, a, rows);
   else
-    hipLaunchKernelGGL((quantize_kernel<T, FMT, false>), grid, dim3(kThreads), 0, st, a, rows);
+    hipLaunchKernelGGL((quantize_kernel<T, FMT, STREAM>), grid, dim3(kThreads), 0, st, a, rows);
   return hipGetLastError();
 }
 
@@ -158,10 +160,12 @@ static hipError_t dequantize_t(const DequantizeArgs& a, hipStream_t st) {
   dim3 grid;
   const Rows rows = split_rows(a.rows, a.cols, &grid);
   const int es = T == PT_F32 ? 4 : 2;
-  if (((reinterpret_cast<uint64_t>(a.y) | static_cast<uint64_t>(a.ldy * es)) & 15) == 0)
-    hipLaunchKernelGGL((dequantize_kernel<T, FMT, true>), grid, dim3(kThreads), 0, st, a, rows);
+  if (((reinterpret_cast<uint64_t>(a.y) | static_cast<uint64_t>(a.ldy * es)) & 15) != 0)
+    hipLaunchKernelGGL((dequantize_kernel<T, FMT, ANY>), grid, dim3(kThreads), 0, st, a, rows);
+  else if (a.rows * a.cols * (es + (FMT == MX_E4M3)) < kLastLevelCache)
+    hipLaunchKernelGGL((dequantize_kernel<T, FMT, ALIGNED>), grid, dim3(kThreads), 0, st, a, rows);
   else
-    hipLaunchKernelGGL((dequantize_kernel<T, FMT, false>), grid, dim3(kThreads), 0, st, a, rows);
+    hipLaunchKernelGGL((dequantize_kernel<T, FMT, STREAM>), grid, dim3(kThreads), 0, st, a, rows);
   return hipGetLastError();
 }
 

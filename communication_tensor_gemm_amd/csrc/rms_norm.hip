@@ -40,8 +40,9 @@ __device__ __forceinline__ float row_sum(float v, float* red, int W) {
 }
 
 // grid: rows over workgroups of rows_per_group rows (W waves each)
-template <int T, int OUT, int V, bool kAligned>
+template <int T, int OUT, int V, int A>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
+  constexpr int kShared = A == ANY ? ANY : ALIGNED;  // what every row reads
   __shared__ float red[kMaxWaves];
   const int wave = threadIdx.x >> 6, groups = (blockDim.x >> 6) / W;
   const int t = static_cast<int>(threadIdx.x) - wave / W * W * 64, span = 64 * W;
@@ -53,7 +54,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
   for (int c = 0; c < V; ++c) {
     const int i = c * span + t;
     x[c].zero();
-    if (live && i < d) x[c].template load<kAligned>(a.x, row * a.ldx + 8 * i, a.cols - 8 * i);
+    if (live && i < d) x[c].template load<A>(a.x, row * a.ldx + 8 * i, a.cols - 8 * i);
   }
   if (a.residual) {
 #pragma unroll
@@ -61,14 +62,14 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
       const int i = c * span + t;
       if (live && i < d) {
         Raw8<T> r;
-        r.template load<kAligned>(a.residual, row * a.ldr + 8 * i, a.cols - 8 * i);
+        r.template load<A>(a.residual, row * a.ldr + 8 * i, a.cols - 8 * i);
         float f[8], g[8];
         x[c].get(f);
         r.get(g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] += g[j];
         x[c].set(f);
-        x[c].template store<kAligned>(a.h, row * a.ldh + 8 * i, a.cols - 8 * i);
+        x[c].template store<A>(a.h, row * a.ldh + 8 * i, a.cols - 8 * i);
       }
     }
   }
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
   for (int c = 0; c < V; ++c) {
     const int i = c * span + t;
     wr[c].zero();
-    if (i < d) wr[c].template load<kAligned>(a.weight, 8 * i, a.cols - 8 * i);
+    if (i < d) wr[c].template load<kShared>(a.weight, 8 * i, a.cols - 8 * i);
   }
   float ss = 0.0f;
 #pragma unroll
@@ -106,14 +107,14 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
     for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
     if constexpr (OUT == NO_SAME) {
       x[c].set(f);
-      x[c].template store<kAligned>(a.y, row * a.ldy + 8 * i, n);
+      x[c].template store<A>(a.y, row * a.ldy + 8 * i, n);
     } else if constexpr (OUT == NO_E4M3) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= a.inv_scale;
       const u32x2 q = pack_e4m3<true>(f);
       uint8_t* y = static_cast<uint8_t*>(a.y) + row * a.ldy + 8 * i;
-      if constexpr (kAligned) {
-        *reinterpret_cast<u32x2*>(y) = q;
+      if constexpr (A != ANY) {
+        store_wide<A>(reinterpret_cast<u32x2*>(y), q);
       } else if (n >= 8) {
         *reinterpret_cast<u32x2_any*>(y) = q;
       } else {
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
       }
     } else {
       constexpr int FMT = OUT == NO_MX_E2M1 ? MX_E2M1 : MX_E4M3;
-      store_block<FMT>(f, static_cast<uint8_t*>(a.y), row * mx_row_bytes(a.cols, FMT), i, a.scales,
+      store_block<FMT, A>(f, static_cast<uint8_t*>(a.y), row * mx_row_bytes(a.cols, FMT), i, a.scales,
                        row * scale_pitch(a.cols));
     }
   }
@@ -143,13 +144,15 @@ static int row_waves(int64_t rows, int d) {
 }
 
 template <int T, int OUT, int V>
-static hipError_t norm_v(const NormArgs& a, int W, bool aligned, hipStream_t st) {
+static hipError_t norm_v(const NormArgs& a, int W, int access, hipStream_t st) {
   const int groups = W >= 4 ? 1 : 4 / W;
   const dim3 grid(static_cast<unsigned>((a.rows + groups - 1) / groups)), block(64 * W * groups);
-  if (aligned)
-    hipLaunchKernelGGL((rms_norm_kernel<T, OUT, V, true>), grid, block, 0, st, a, W);
+  if (access == STREAM)
+    hipLaunchKernelGGL((rms_norm_kernel<T, OUT, V, STREAM>), grid, block, 0, st, a, W);
+  else if (access == ALIGNED)
+    hipLaunchKernelGGL((rms_norm_kernel<T, OUT, V, ALIGNED>), grid, block, 0, st, a, W);
   else
-    hipLaunchKernelGGL((rms_norm_kernel<T, OUT, V, false>), grid, block, 0, st, a, W);
+    hipLaunchKernelGGL((rms_norm_kernel<T, OUT, V, ANY>), grid, block, 0, st, a, W);
   return hipGetLastError();
 }
 
@@ -163,10 +166,11 @@ static hipError_t norm_t(const NormArgs& a, hipStream_t st) {
          static_cast<uint64_t>(a.ldh * es);
   if (OUT == NO_SAME) m |= reinterpret_cast<uint64_t>(a.y) | static_cast<uint64_t>(a.ldy * es);
   if (OUT == NO_E4M3) m |= (reinterpret_cast<uint64_t>(a.y) | static_cast<uint64_t>(a.ldy)) << 1;  // 8-byte stores
-  const bool aligned = (m & 15) == 0 && a.cols % 8 == 0;
-  if (v <= 1) return norm_v<T, OUT, 1>(a, W, aligned, st);
-  if (v <= 2) return norm_v<T, OUT, 2>(a, W, aligned, st);
-  return norm_v<T, OUT, 4>(a, W, aligned, st);
+  const int64_t bytes = a.rows * a.cols * ((a.residual ? 3 : 1) * es + (OUT == NO_SAME ? es : 1));
+  const int access = (m & 15) != 0 || a.cols % 8 != 0 ? ANY : bytes < kLastLevelCache ? ALIGNED : STREAM;
+  if (v <= 1) return norm_v<T, OUT, 1>(a, W, access, st);
+  if (v <= 2) return norm_v<T, OUT, 2>(a, W, access, st);
+  return norm_v<T, OUT, 4>(a, W, access, st);
 }
 
 template <int T>
@@ -191,8 +195,9 @@ static hipError_t norm_out(int out, const NormArgs& a, hipStream_t st) {
 // the current row's sum crosses the waves; longer rows have no registers for
 // that, and above 16384 columns the row itself is read again (from the L2)
 // after its sum.
-template <int T, int V, bool kAligned>
+template <int T, int V, int A>
 __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArgs a, int W) {
+  constexpr int kShared = A == ANY ? ANY : ALIGNED;
   __shared__ float red[2][kMaxWaves];
   const int wave = threadIdx.x >> 6, groups = (blockDim.x >> 6) / W;
   const int t = static_cast<int>(threadIdx.x) - wave / W * W * 64, span = 64 * W;
@@ -209,7 +214,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArg
   Raw8<T> wr;  // the weight: kept if it is one piece
   auto weight = [&](int i) {
     wr.zero();
-    if (i < d) wr.template load<kAligned>(a.weight, 8 * i, a.cols - 8 * i);
+    if (i < d) wr.template load<kShared>(a.weight, 8 * i, a.cols - 8 * i);
   };
   if constexpr (V == 1) weight(t);
   // all groups of the workgroup make the same number of turns (they share the barrier)
@@ -224,9 +229,9 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArg
     pd.zero();
     if (r < a.rows && i < d) {
       const int n = a.cols - 8 * i;
-      py.template load<kAligned>(a.dy, r * a.lddy + 8 * i, n);
-      ph.template load<kAligned>(a.h, r * a.ldh + 8 * i, n);
-      if (a.dh) pd.template load<kAligned>(a.dh, r * a.lddh + 8 * i, n);
+      py.template load<A>(a.dy, r * a.lddy + 8 * i, n);
+      ph.template load<A>(a.h, r * a.ldh + 8 * i, n);
+      if (a.dh) pd.template load<A>(a.dh, r * a.lddh + 8 * i, n);
     }
   };
   auto scale = [&](int64_t r) { return r < a.rows ? a.rstd[r] : 0.0f; };
@@ -298,7 +303,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArg
       for (int j = 0; j < 8; ++j) o[j] = __builtin_fmaf(xs[q][j], k3, __builtin_fmaf(yw[q][j], s, e[j]));
       Raw8<T> out;
       out.set(o);
-      out.template store<kAligned>(a.dx, row * a.lddx + 8 * i, a.cols - 8 * i);
+      out.template store<A>(a.dx, row * a.lddx + 8 * i, a.cols - 8 * i);
     }
     row += step;
   }
@@ -327,7 +332,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArg
     if (i >= d) continue;
     Raw8<PT_F32> out;
     out.set(dw[c]);
-    out.template store<false>(a.partial, static_cast<int64_t>(blockIdx.x) * a.cols + 8 * i, a.cols - 8 * i);
+    out.template store<ANY>(a.partial, static_cast<int64_t>(blockIdx.x) * a.cols + 8 * i, a.cols - 8 * i);
   }
 }
 
@@ -367,12 +372,14 @@ static void backward_shape(int type, int64_t rows, int64_t cols, int* W, int* gr
 }
 
 template <int T, int V>
-static void backward_v(const NormBackwardArgs& a, int W, int groups, int64_t blocks, bool aligned, hipStream_t st) {
+static void backward_v(const NormBackwardArgs& a, int W, int groups, int64_t blocks, int access, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * W * groups);
-  if (aligned)
-    hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, true>), grid, block, 0, st, a, W);
+  if (access == STREAM)
+    hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, STREAM>), grid, block, 0, st, a, W);
+  else if (access == ALIGNED)
+    hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, ALIGNED>), grid, block, 0, st, a, W);
   else
-    hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, false>), grid, block, 0, st, a, W);
+    hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, ANY>), grid, block, 0, st, a, W);
 }
 
 template <int T>
@@ -382,19 +389,21 @@ static hipError_t backward_t(const NormBackwardArgs& a, hipStream_t st) {
                reinterpret_cast<uint64_t>(a.weight) | static_cast<uint64_t>(a.lddy) * es |
                static_cast<uint64_t>(a.ldh) * es | static_cast<uint64_t>(a.lddx) * es;
   if (a.dh) m |= reinterpret_cast<uint64_t>(a.dh) | static_cast<uint64_t>(a.lddh) * es;
-  const bool aligned = (m & 15) == 0 && a.cols % 8 == 0;
+  const int64_t bytes = a.rows * a.cols * static_cast<int64_t>(es) * (a.dh ? 4 : 3);
   int W, groups;
   int64_t blocks;
   backward_shape(T, a.rows, a.cols, &W, &groups, &blocks);
   const int d = (a.cols + 7) / 8, v = (d + 64 * W - 1) / (64 * W);
+  // a row that is read twice (above 16384 columns) has to be found in the cache
+  const int access = (m & 15) != 0 || a.cols % 8 != 0 ? ANY : bytes < kLastLevelCache || v > 2 ? ALIGNED : STREAM;
   if (blocks == 0)
     ;  // no rows: the second kernel writes zeros
   else if (v <= 1)
-    backward_v<T, 1>(a, W, groups, blocks, aligned, st);
+    backward_v<T, 1>(a, W, groups, blocks, access, st);
   else if (v <= 2)
-    backward_v<T, 2>(a, W, groups, blocks, aligned, st);
+    backward_v<T, 2>(a, W, groups, blocks, access, st);
   else
-    backward_v<T, 4>(a, W, groups, blocks, aligned, st);
+    backward_v<T, 4>(a, W, groups, blocks, access, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(rms_norm_dweight_kernel, dim3(static_cast<unsigned>((a.cols + 63) / 64)), dim3(1024), 0, st,

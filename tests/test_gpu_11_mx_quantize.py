@@ -153,3 +153,25 @@ def test_on_a_stream_of_its_own_and_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert np.array_equal(codes.cpu().numpy(), want) and np.array_equal(scales.cpu().numpy(), want_s)
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "E4M3"])
+@pytest.mark.parametrize("typ", ["BF16", "F32"])
+def test_matrices_past_the_cache_equal_their_parts(fmt, typ):
+    """Above the last-level cache's size the accesses go past the caches: the same bytes."""
+    import torch
+    rows, cols = 20000, 8224
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16 if typ == "BF16" else torch.float32)
+    codes, scales = buffers(rows, cols, fmt)
+    dg.dist_gemm_mx_quantize(x, fmt, codes, scales)
+    y = torch.empty_like(x)
+    dg.dist_gemm_mx_dequantize(codes, scales, fmt, y)
+    for lo in range(0, rows, 4000):
+        c, s = buffers(4000, cols, fmt)
+        part = x[lo:lo + 4000]
+        dg.dist_gemm_mx_quantize(part, fmt, c, s)
+        z = torch.empty_like(part)
+        dg.dist_gemm_mx_dequantize(c, s, fmt, z)
+        assert torch.equal(c, codes[lo:lo + 4000]) and torch.equal(s, scales[lo:lo + 4000])
+        assert torch.equal(z, y[lo:lo + 4000])

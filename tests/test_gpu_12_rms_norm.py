@@ -315,3 +315,53 @@ def test_refusals_of_tensors():
         ws = torch.empty(16, dtype=torch.uint8, device="cuda")
         dg.dist_gemm_rms_norm_backward(x, x, torch.ones(4, device="cuda"), w, y, torch.empty(64, device="cuda"), ws)
     assert ei.value.status == -1
+
+
+@pytest.mark.parametrize("typ", ["BF16", "F32"])
+@pytest.mark.parametrize("out", ["SAME", "E4M3", "MX_E2M1", "MX_E4M3"])
+def test_matrices_past_the_cache_equal_their_parts(typ, out):
+    """Above the last-level cache's size the accesses go past the caches: the same bytes."""
+    import torch
+    rows, cols = 9000, 8224
+    t = torch_type(typ)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, r = (torch.randn(rows, cols, generator=g, device="cuda").to(t) for _ in range(2))
+    w = torch.randn(cols, generator=g, device="cuda").to(t)
+
+    def run(x, r):
+        n = x.size(0)
+        y = torch.empty((n, cols // 2 if out == "MX_E2M1" else cols), device="cuda", dtype=t if out == "SAME" else torch.uint8)
+        s = torch.empty((n, mx.scale_pitch(cols)), dtype=torch.uint8, device="cuda") if out.startswith("MX") else None
+        h, rstd = torch.empty_like(x), torch.empty(n, device="cuda")
+        dg.dist_gemm_rms_norm(x, w, y, output=out, residual=r, h=h, rstd=rstd, scales=s, scale=0.1)
+        return [v for v in (y, h, rstd, s) if v is not None]
+
+    whole = run(x, r)
+    for lo in range(0, rows, 2250):
+        part = run(x[lo:lo + 2250], r[lo:lo + 2250])
+        assert all(torch.equal(p, v[lo:lo + 2250]) for p, v in zip(part, whole))
+
+
+@pytest.mark.parametrize("typ", ["BF16", "F32"])
+def test_gradients_past_the_cache_equal_their_parts(typ):
+    import torch
+    rows, cols = 9000, 8224 if typ == "BF16" else 8000
+    t = torch_type(typ)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    h, dy, dh = (torch.randn(rows, cols, generator=g, device="cuda").to(t) for _ in range(3))
+    w, rstd = torch.randn(cols, generator=g, device="cuda").to(t), torch.rand(rows, generator=g, device="cuda")
+
+    def run(lo, hi):
+        dx, dw = torch.empty_like(h[lo:hi]), torch.empty(cols, device="cuda")
+        ws = torch.empty(dg.dist_gemm_rms_norm_workspace(hi - lo, cols), dtype=torch.uint8, device="cuda")
+        dg.dist_gemm_rms_norm_backward(dy[lo:hi], h[lo:hi], rstd[lo:hi], w, dx, dw, ws, dh=dh[lo:hi])
+        return dx, dw.double()
+
+    dx, dw = run(0, rows)
+    total = torch.zeros(cols, dtype=torch.float64, device="cuda")
+    for lo in range(0, rows, 1500):
+        part, d = run(lo, lo + 1500)
+        assert torch.equal(part, dx[lo:lo + 1500])
+        total += d
+    size = (dy.double() * h.double() * rstd.double()[:, None]).abs().sum(0)
+    assert bool(((dw - total).abs() <= (rows / 2 + 24) * U * size).all())
