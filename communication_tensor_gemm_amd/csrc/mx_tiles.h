@@ -169,5 +169,13 @@ __device__ __forceinline__ bool wide_rows(const MxGemmArgs& a) {
   return ((reinterpret_cast<uint64_t>(a.D) | static_cast<uint64_t>(a.ldd) * es) & (4 * es - 1)) == 0;
 }
 
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+// The caller has waited for what the other waves must see; no memory fence.
+__device__ __forceinline__ void barrier_only() { asm volatile("s_barrier" ::: "memory"); }
+
 }  // namespace mx
 }  // namespace dg
