@@ -28,6 +28,14 @@
 // With one workgroup per CU, prologue and epilogue of a tile took 18 us of
 // 127 (E2M1, K = 16384) when nothing overlapped them.
 //
+// Few tiles.  Where no CU has a second tile, a slab's 16 or so MFMAs per wave
+// do not cover its loads' latency and its other instructions (0.7 us per slab,
+// deeper stages or not).  With a long K, two groups of four waves then compute
+// half of a tile's K each, with stages of their own, and the second group's
+// sums go to the first through LDS at the end: 128 x 13312 x 16384 E2M1 48.4 ->
+// 42.6 us.  That end costs 1.5 us, so for K up to 4096 one group is as fast or
+// faster (256 x 8192 x 3584: 12.6 us, with two 14.1).
+//
 // Operand layout (see mx_gemm_rows.hip for the other MFMA's): lane l has row
 // l % 32 and, with h = l / 32, an E2M1 block of 32 elements, or of E4M3
 // elements 16 h .. + 15 and 32 + 16 h .. + 15 of 64.  Its scale is that of
@@ -189,20 +197,23 @@ __device__ __forceinline__ Place place_of(Tiles t, int32_t at) {
 }
 
 // The wave's block of D from its accumulators.  A lane holds, of block (i,
-// j), row l % 32 and columns 8 g + 4 h + 0 .. 3 (g = 0 .. 3).  A whole bf16
-// block without C: the two halves of the wave exchange their fours of g and
+// j), row l % 32 and columns 8 g + 4 h + 0 .. 3 (g = 0 .. 3).  Whole columns of
+// bf16 without C: the two halves of the wave exchange their fours of g and
 // g + 1, so that each lane has eight neighbouring columns and an instruction
-// stores 32 rows of 32 bytes (kStores instructions in all, and true is
-// returned); else four columns at a time.  No LDS: the next tile's slabs are
-// in it.
+// stores 32 rows of 32 bytes, those past the last row out of the descriptor's
+// range (kStores instructions in all, and true is returned); else four columns
+// at a time.  No LDS: the next tile's slabs are in it.
 template <bool kBf16, int NBM, int NBN>
 __device__ __forceinline__ bool store_block_of(const MxGemmArgs& p, const Place& at, int wm, int wn, int lane,
                                                f32x16 (&acc)[NBM][NBN]) {
   constexpr int WM = 32 * NBM, WN = 32 * NBN;
   const int32_t wrow = wm * WM, wcol = wn * WN;
-  const bool whole = kBf16 && at.rows - wrow >= WM && at.cols - wcol >= WN && p.beta == 0.0f &&
+  // (a tile's rows within 2 GiB: offsets of 32 bits)
+  const bool whole = kBf16 && at.cols - wcol >= WN && p.beta == 0.0f && p.ldd < (1 << 22) &&
                      ((reinterpret_cast<uint64_t>(p.D) | (static_cast<uint64_t>(p.ldd) * 2)) & 15) == 0;
   const bool wide = wide_rows<kBf16>(p);
+  const uint32_t pitch = whole ? static_cast<uint32_t>(p.ldd) * 2 : 0;
+  const auto rD = make_rsrc(static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(at.row0) * p.ldd + at.n0) * 2, at.rows * pitch);
 #pragma unroll
   for (int i = 0; i < NBM; ++i)
 #pragma unroll
@@ -228,13 +239,13 @@ __device__ __forceinline__ bool store_block_of(const MxGemmArgs& p, const Place&
           }
           w[g] = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
         }
-        const auto d = (global_ptr<uint16_t>)p.D + static_cast<int64_t>(at.row0 + r) * p.ldd + at.n0 + c0 + 8 * eh;
+        const uint32_t d = r * pitch + (c0 + 8 * eh) * 2;
 #pragma unroll
         for (int g = 0; g < 4; g += 2) {
           // the upper half's fours of g against the lower half's of g + 1
           const auto x = __builtin_amdgcn_permlane32_swap(w[g][0], w[g + 1][0], false, false);
           const auto y = __builtin_amdgcn_permlane32_swap(w[g][1], w[g + 1][1], false, false);
-          *(global_ptr<u32x4>)(d + 8 * g) = u32x4{x[0], y[0], x[1], y[1]};
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{x[0], y[0], x[1], y[1]}, rD, d + 16 * g, 0, 0);
         }
       } else if (r < at.rows) {
 #pragma unroll
@@ -249,11 +260,14 @@ __device__ __forceinline__ bool store_block_of(const MxGemmArgs& p, const Place&
   return whole;
 }
 
-// A workgroup's share of the launch.
-template <bool A8, bool kBf16, int NBM, int NBN>
-__device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* smem) {
+// A workgroup's share of the launch.  KG = 2: of its one tile, two groups of four
+// waves compute half of K each.
+template <bool A8, bool kBf16, int NBM, int NBN, int KG>
+__device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* const all_smem) {
   using G = Geo<A8, NBM, NBN>;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  uint8_t* const smem = all_smem + kg * G::kLds;
   const int wm = wave >> 1, wn = wave & 1, h = lane >> 5;
   const Tiles tiles = all_tiles<G>(p);
   int32_t at = tiles.begin;
@@ -262,8 +276,13 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* smem) {
   Place cur = place_of<G>(tiles, at), next = place_of<G>(tiles, at + tiles.step);
   const uint32_t lda = static_cast<uint32_t>(A8 ? p.K : p.K / 2), ldb = static_cast<uint32_t>(p.K / 2);
   const uint32_t pitch = static_cast<uint32_t>(scale_pitch(p.K));
-  const int KT = (p.K + G::kSlabK - 1) / G::kSlabK, KC = (p.K + 511) / 512;
-  const bool partial = KT * G::kSlabK != p.K;
+  // KG = 2: the first group takes whole chunks of scales, the second what is
+  // left, K elements from kfrom on, and slabs of zeros up to the first one's number
+  const int each = (p.K + 512 * KG - 1) / (512 * KG) * 512, kfrom = kg * each;
+  const int K = KG == 1 ? static_cast<int>(p.K) : min(static_cast<int>(p.K) - kfrom, each);
+  const int KT = ((KG == 1 ? K : each) + G::kSlabK - 1) / G::kSlabK, KC = ((KG == 1 ? K : each) + 511) / 512;
+  const bool partial = KT * G::kSlabK != K;
+  const uint32_t afrom = A8 ? kfrom : kfrom / 2, bfrom = kfrom / 2, sfrom = kfrom / kMxBlock;  // bytes of a row
   uint8_t* const scales = smem + G::kStages * G::kStage;
 
   // ---- loads.  The loader walks the workgroup's stream of slabs; lkt is its
@@ -271,15 +290,16 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* smem) {
   __amdgpu_buffer_rsrc_t rA, rB, rS;
   auto slabs_of = [&](const Place& q) {
     const MxGemmArgs p = fresh_args();
-    rA = make_rsrc(p.A + static_cast<int64_t>(q.row0) * lda, q.rows * lda);
-    rB = make_rsrc(p.B + (q.b_row0 + q.n0) * ldb, q.cols * ldb);
+    // no tile: no bytes, also with the second half's offset
+    rA = make_rsrc(p.A + static_cast<int64_t>(q.row0) * lda + afrom, KG == 1 || q.rows ? q.rows * lda - afrom : 0);
+    rB = make_rsrc(p.B + (q.b_row0 + q.n0) * ldb + bfrom, KG == 1 || q.rows ? q.cols * ldb - bfrom : 0);
   };
   // waves 0, 1 load scales of A, 2, 3 of B
   const bool scale_a = wave < 2;
   auto scales_of = [&](const Place& q) {
     const MxGemmArgs p = fresh_args();
-    rS = make_rsrc(scale_a ? p.As + static_cast<int64_t>(q.row0) * pitch : p.Bs + (q.b_row0 + q.n0) * pitch,
-                   (scale_a ? q.rows : q.cols) * pitch);
+    rS = make_rsrc((scale_a ? p.As + static_cast<int64_t>(q.row0) * pitch : p.Bs + (q.b_row0 + q.n0) * pitch) + sfrom,
+                   KG == 1 || q.rows ? (scale_a ? q.rows : q.cols) * pitch - sfrom : 0);
   };
   // lane offsets: 128-byte rows in even and odd blocks of 8 rows, 64-byte rows in blocks of 16
   const int piece = lane & 3, r16 = lane >> 2;
@@ -294,17 +314,17 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* smem) {
   const uint32_t gs = static_cast<uint32_t>((scale_a ? wave : wave - 2) * 64 * G::LS + lane) * pitch;
   int lkt = 0;
   // before the loads of slab lkt, K not a multiple of the slab: the last
-  // slab's pieces past K out of range, the first slab's back in
+  // slabs' pieces past K out of range, the first slab's back in
   auto mask = [&]() {
-    if (!partial || (lkt != 0 && lkt != KT - 1)) return;
+    const bool last = KG == 1 ? lkt == KT - 1 : (lkt + 1) * G::kSlabK > K;
+    if (!partial || (lkt != 0 && !last)) return;
     const int k0 = lkt * G::kSlabK;
-    const bool last = lkt == KT - 1;
 #pragma unroll
     for (int odd = 0; odd < 2; ++odd) {
       const int ka = k0 + byte_in_slab(odd) * (A8 ? 1 : 2);
       const int kb = A8 ? k0 + 32 * (piece ^ row_perm(r16)) : ka;
-      ga[odd] = (ga[odd] & ~kOutOfRange) | (last && ka >= p.K ? kOutOfRange : 0u);
-      gb[odd] = (gb[odd] & ~kOutOfRange) | (last && kb >= p.K ? kOutOfRange : 0u);
+      ga[odd] = (ga[odd] & ~kOutOfRange) | (last && ka >= K ? kOutOfRange : 0u);
+      gb[odd] = (gb[odd] & ~kOutOfRange) | (last && kb >= K ? kOutOfRange : 0u);
     }
   };
   constexpr int kLoads = G::LA + G::LB;
@@ -395,8 +415,8 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* smem) {
   // a scale byte past K may hold anything, also the NaN scale: the bytes of
   // dword `dword` of slab kt that count
   auto keep_of = [&](int kt, int dword) -> uint32_t {
-    if (!partial || kt != KT - 1) return ~0u;
-    const int left = p.K - kt * G::kSlabK - 128 * dword;
+    if (!partial || (KG == 1 ? kt != KT - 1 : (kt + 1) * G::kSlabK <= K)) return ~0u;
+    const int left = K - kt * G::kSlabK - 128 * dword;
     return left >= 128 ? ~0u : left <= 0 ? 0u : (1u << (left / 4)) - 1u;
   };
   auto make_scale = [&](int set, int r, int dword, uint32_t keep) {
@@ -557,10 +577,38 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* smem) {
       for (int i = 0; i < NBM; ++i)
 #pragma unroll
         for (int j = 0; j < NBN; ++j) asm volatile("" : "+a"(acc[i][j]));
+      if constexpr (KG == 2) {
+        // the second group's sums to the first, through the second's stages: all
+        // of its slabs have been read, and no load into them is under way
+        static_assert(G::kStages * G::kStage >= NBM * NBN * 4 * 4096, "room for the sums");
+        wait_vmcnt<0>();
+        barrier_only();
+        f32x4* const sums = reinterpret_cast<f32x4*>(all_smem + G::kLds) + wave * NBM * NBN * 4 * 64 + lane;
+        if (kg == 1) {
+#pragma unroll
+          for (int b = 0; b < NBM * NBN; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const f32x16& v = acc[b / NBN][b % NBN];
+              sums[(b * 4 + g) * 64] = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+            }
+        }
+        wait_lgkmcnt0();
+        barrier_only();
+        if (kg == 1) return;
+#pragma unroll
+        for (int b = 0; b < NBM * NBN; ++b)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x4 v = sums[(b * 4 + g) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[b / NBN][b % NBN][4 * g + e] += v[e];
+          }
+      }
       int elane = lane;  // the epilogue's addresses are not hoisted above the loop
       asm volatile("" : "+v"(elane));
       behind = store_block_of<kBf16, NBM, NBN>(fresh_args(), cur, wm, wn, elane, acc);
-      if (next.rows == 0) return;
+      if (KG == 2 || next.rows == 0) return;
       clear();
       at += tiles.step;
       cur = next;
@@ -578,11 +626,11 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* smem) {
   }
 }
 
-template <bool A8, bool kBf16, int NBM, int NBN>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NBM* NBN == 16 ? 1 : 2, NBM* NBN == 16 ? 1 : 2)))
+template <bool A8, bool kBf16, int NBM, int NBN, int KG>
+__global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(NBM* NBN == 16 ? 1 : 2, NBM* NBN == 16 ? 1 : 2)))
 void mx_gemm_tile_kernel(MxGemmArgs p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[Geo<A8, NBM, NBN>::kLds];
-  run_tiles<A8, kBf16, NBM, NBN>(p, smem);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[KG * Geo<A8, NBM, NBN>::kLds];
+  run_tiles<A8, kBf16, NBM, NBN, KG>(p, smem);
 }
 
 template <bool A8, bool kBf16, int NBM, int NBN>
@@ -593,7 +641,14 @@ static hipError_t tile_t(const MxGemmArgs& a, hipStream_t st) {
   if (T > INT32_MAX / 2) return hipErrorInvalidConfiguration;
   const int64_t most = static_cast<int64_t>(a.cus) * G::kWgs;
   const int64_t grid = ((T < most ? T : most) + kXcds - 1) / kXcds * kXcds;
-  hipLaunchKernelGGL((mx_gemm_tile_kernel<A8, kBf16, NBM, NBN>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
+  const dim3 wgs(static_cast<unsigned>(grid));
+  if constexpr (NBM * NBN < 16) {
+    if (T <= a.cus && a.K > 4096) {  // "Few tiles" above
+      hipLaunchKernelGGL((mx_gemm_tile_kernel<A8, kBf16, NBM, NBN, 2>), wgs, dim3(512), 0, st, a);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((mx_gemm_tile_kernel<A8, kBf16, NBM, NBN, 1>), wgs, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
