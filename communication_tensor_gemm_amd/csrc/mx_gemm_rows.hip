@@ -323,14 +323,23 @@ static hipError_t rows_t(const MxGemmArgs& a, hipStream_t st) {
 
 // Few rows stream the weights; from 65 rows on (of a group, on average), tiles
 // (128 x 13312 x 16384, E4M3: 58 us against 100 in two passes of 64 rows).
+//
+// Tiles of 256 x 256 read the operands half as often, tiles of 128 x 128 leave
+// fewer CUs idle in the last round.  A round of the larger ones takes as long
+// as three of the smaller ones with one per CU (M x 8192 x 4096, E4M3, larger /
+// smaller: M = 1024 49 / 38 us, 1536 53 / 55, 2048 62 / 73, 2304 95 / 87, 4096
+// 117 / 142).  A group's last tile is taken as half full.
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t st) {
   if (a.M == 0) return hipSuccess;
   const int64_t rows = a.offsets ? a.M / a.groups : a.M;
   if (rows <= 16) return mx::rows_t<1>(a, st);
   if (rows <= 32) return mx::rows_t<2>(a, st);
   if (rows <= 64) return mx::rows_t<4>(a, st);
-  const int64_t tiles = ((rows + 255) / 256) * ((a.N + 255) / 256) * (a.offsets ? a.groups : 1);
-  return launch_mx_gemm_tile(tiles >= 192 ? 256 : 128, a, st);
+  auto rounds = [&](int64_t size) {
+    const int64_t row_tiles = a.offsets ? a.M / size + (a.groups + 1) / 2 : (a.M + size - 1) / size;
+    return (row_tiles * ((a.N + size - 1) / size) + a.cus - 1) / a.cus;
+  };
+  return launch_mx_gemm_tile(3 * rounds(256) <= rounds(128) ? 256 : 128, a, st);
 }
 
 }  // namespace dg
