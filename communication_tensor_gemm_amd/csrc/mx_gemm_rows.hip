@@ -5,7 +5,7 @@
 // into the registers of the MFMA that multiplies them, 16 x 16 x 128 with
 // per-block scales (v_mfma_scale_f32_16x16x128_f8f6f4).  The first MFMA
 // operand is B and the second A, so a lane ends with four neighbouring columns
-// of one row of D.  The workgroup's eight waves split K among them in chunks of
+// of one row of D.  The workgroup's waves split K among them in chunks of
 // 512 and add their sums through LDS in a fixed order.
 //
 // Loads.  A vector load runs at 64 bytes a cycle where four neighbouring lanes
@@ -42,7 +42,6 @@ namespace dg {
 namespace mx {
 
 constexpr int kChunk = 512;  // elements of K per step of a wave
-constexpr int kWaves = 8;
 constexpr int kLdsA = 48 * 1024;      // bytes of A, its scales and their padding in LDS
 constexpr int kPadA = 64, kPadS = 16;  // between rows: the 16 rows of a read on distinct banks
 
@@ -74,7 +73,7 @@ __device__ __forceinline__ void transpose_quads(i32x4 (&v)[4], bool odd, bool hi
   }
 }
 
-template <int MB, int NB, bool A8, bool kBf16, bool kLds>
+template <int MB, int NB, bool A8, bool kBf16, bool kLds, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void mx_gemm_rows_kernel(MxGemmArgs a, int step) {  // step: columns of a workgroup
   constexpr int kAL = A8 ? 8 : 4;  // 16-byte pieces of a lane per chunk of a row of A
   constexpr int kAhead = NB == 1 ? 2 : 1;  // chunks asked for before they are multiplied (twice as many: no faster)
@@ -281,8 +280,8 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemm_rows_kernel(MxGemmArgs a,
   }
 }
 
-template <int MB, int NB, bool kLds>
-static hipError_t rows_lds_t(const MxGemmArgs& a, hipStream_t st) {
+template <int MB, int NB, bool kLds, int kWaves>
+static hipError_t rows_waves_t(const MxGemmArgs& a, hipStream_t st) {
   const int64_t tiles = a.offsets ? most_group_tiles(a.M, a.groups, 16 * MB) : (a.M + 16 * MB - 1) / (16 * MB);
   int step = 16 * NB;
   if (!a.offsets) {
@@ -295,16 +294,25 @@ static hipError_t rows_lds_t(const MxGemmArgs& a, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kWaves);
   if (a.a_format == MX_E4M3) {
     if (a.out_bf16)
-      hipLaunchKernelGGL((mx_gemm_rows_kernel<MB, NB, true, true, kLds>), grid, block, 0, st, a, step);
+      hipLaunchKernelGGL((mx_gemm_rows_kernel<MB, NB, true, true, kLds, kWaves>), grid, block, 0, st, a, step);
     else
-      hipLaunchKernelGGL((mx_gemm_rows_kernel<MB, NB, true, false, kLds>), grid, block, 0, st, a, step);
+      hipLaunchKernelGGL((mx_gemm_rows_kernel<MB, NB, true, false, kLds, kWaves>), grid, block, 0, st, a, step);
   } else {
     if (a.out_bf16)
-      hipLaunchKernelGGL((mx_gemm_rows_kernel<MB, NB, false, true, kLds>), grid, block, 0, st, a, step);
+      hipLaunchKernelGGL((mx_gemm_rows_kernel<MB, NB, false, true, kLds, kWaves>), grid, block, 0, st, a, step);
     else
-      hipLaunchKernelGGL((mx_gemm_rows_kernel<MB, NB, false, false, kLds>), grid, block, 0, st, a, step);
+      hipLaunchKernelGGL((mx_gemm_rows_kernel<MB, NB, false, false, kLds, kWaves>), grid, block, 0, st, a, step);
   }
   return hipGetLastError();
+}
+
+// Eight waves to a workgroup; four where there are many workgroups of few
+// chunks each, so that more of them are under way at once (by group, 64 rows, 32
+// x 2048 x 4096, E4M3: 21.6 us, with eight 25.5; dense at 8192 x 8192 and one row
+// eight take 9.5 us, four 11.3).
+template <int MB, int NB, bool kLds>
+static hipError_t rows_lds_t(const MxGemmArgs& a, hipStream_t st) {
+  return a.offsets && a.K <= 8 * kChunk ? rows_waves_t<MB, NB, kLds, 4>(a, st) : rows_waves_t<MB, NB, kLds, 8>(a, st);
 }
 
 // Rows that fit into LDS leave a wave little else to load than B: 16 columns,

