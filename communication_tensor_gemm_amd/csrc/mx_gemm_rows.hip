@@ -285,8 +285,9 @@ static hipError_t rows_waves_t(const MxGemmArgs& a, hipStream_t st) {
   const int64_t tiles = a.offsets ? most_group_tiles(a.M, a.groups, 16 * MB) : (a.M + 16 * MB - 1) / (16 * MB);
   int step = 16 * NB;
   if (!a.offsets) {
-    const int64_t per = static_cast<int64_t>(step) * a.cus, all = (a.N + per - 1) / per * a.cus;
-    const int64_t even = (a.N + all - 1) / all;
+    // the columns' share of what makes row tiles x column tiles a multiple of the CUs
+    const int64_t per = static_cast<int64_t>(step) * a.cus, all = (a.N * tiles + per - 1) / per * a.cus / tiles;
+    const int64_t even = all > 0 ? (a.N + all - 1) / all : step;
     step = static_cast<int>(even < 4 ? 4 : even);
   }
   const int64_t blocks = tiles * ((a.N + step - 1) / step);
@@ -332,6 +333,11 @@ static hipError_t rows_t(const MxGemmArgs& a, hipStream_t st) {
 // Few rows stream the weights; from 65 rows on (of a group, on average), tiles
 // (128 x 13312 x 16384, E4M3: 58 us against 100 in two passes of 64 rows).
 //
+// Few tiles would leave most CUs idle: then 32 rows at a time here, K split over
+// a workgroup's waves (E4M3, this / tiles of 128: 126 x 113 x 15168 12 / 49 us,
+// 128 x 512 x 1024 6.2 / 7.7, 512 x 1024 x 3584 10.5 / 16.6; 512 x 2048, 64
+// tiles: K = 3584 18.2 / 16.9, 15168 50 / 62).
+//
 // Tiles of 256 x 256 read the operands half as often, tiles of 128 x 128 leave
 // fewer CUs idle in the last round.  A round of the larger ones takes as long
 // as three of the smaller ones with one per CU (M x 8192 x 4096, E4M3, larger /
@@ -343,10 +349,12 @@ hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t st) {
   if (rows <= 16) return mx::rows_t<1>(a, st);
   if (rows <= 32) return mx::rows_t<2>(a, st);
   if (rows <= 64) return mx::rows_t<4>(a, st);
-  auto rounds = [&](int64_t size) {
+  auto tiles = [&](int64_t size) {
     const int64_t row_tiles = a.offsets ? a.M / size + (a.groups + 1) / 2 : (a.M + size - 1) / size;
-    return (row_tiles * ((a.N + size - 1) / size) + a.cus - 1) / a.cus;
+    return row_tiles * ((a.N + size - 1) / size);
   };
+  auto rounds = [&](int64_t size) { return (tiles(size) + a.cus - 1) / a.cus; };
+  if (tiles(128) <= a.cus / 8 || (tiles(128) <= a.cus / 4 && a.K > 4096)) return mx::rows_lds_t<2, 2, false>(a, st);
   return launch_mx_gemm_tile(3 * rounds(256) <= rounds(128) ? 256 : 128, a, st);
 }
 
