@@ -36,6 +36,7 @@
 // E4M3 operand's lane holds elements 16 (l / 16) .. + 15 in its first four
 // registers and 64 + 16 (l / 16) .. + 15 in the last four.  The scale byte
 // that a lane passes is that of block l / 16 of its row, in both cases.
+#include "mx_shape.h"
 #include "mx_tiles.h"
 
 namespace dg {
@@ -283,13 +284,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemm_rows_kernel(MxGemmArgs a,
 template <int MB, int NB, bool kLds, int kWaves>
 static hipError_t rows_waves_t(const MxGemmArgs& a, hipStream_t st) {
   const int64_t tiles = a.offsets ? most_group_tiles(a.M, a.groups, 16 * MB) : (a.M + 16 * MB - 1) / (16 * MB);
-  int step = 16 * NB;
-  if (!a.offsets) {
-    // the columns' share of what makes row tiles x column tiles a multiple of the CUs
-    const int64_t per = static_cast<int64_t>(step) * a.cus, all = (a.N * tiles + per - 1) / per * a.cus / tiles;
-    const int64_t even = all > 0 ? (a.N + all - 1) / all : step;
-    step = static_cast<int>(even < 4 ? 4 : even);
-  }
+  const int step = a.offsets ? 16 * NB : rows_step(a.N, tiles, 16 * NB, a.cus);
   const int64_t blocks = tiles * ((a.N + step - 1) / step);
   if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kWaves);
