@@ -40,26 +40,37 @@ struct GroupTile {
 };
 
 // Row tile u (of height tm) of the groups' rows, groups in order, each with
-// ceil(rows / tm) tiles.  Offsets are clamped to [0, M] and to be ascending,
-// so that wrong ones cannot reach past the operands.  The wave's 64 lanes
-// take 64 groups at a time: a scan of their tile counts, then a ballot.
+// ceil(rows / tm) tiles.  Offsets are clamped to [0, M] and to be ascending (one
+// below an earlier one counts as that one), so that wrong ones cannot reach past
+// the operands, no row is in two groups, and the tiles are no more than the
+// launch was made for.  The wave's 64 lanes take 64 groups at a time: a scan of
+// their tile counts, then a ballot.
 // Every lane of the wave calls it with the same arguments.  total: all tiles.
 __device__ __forceinline__ int32_t group_bound(const int32_t* offsets, int32_t i, int32_t M) {
   return min(max(((global_ptr<const int32_t>)offsets)[i], 0), M);
 }
 
 // 64 groups, one per lane: their rows lo .. hi - 1 and the tiles of the
-// groups up to and including the lane's.
+// groups up to and including the lane's.  from: the end of the groups before.
 struct GroupLanes {
   int32_t lo, hi, incl;
 };
 __device__ __forceinline__ GroupLanes load_groups(const int32_t* offsets, int32_t groups, int32_t M, int32_t tm,
-                                                  int32_t base = 0) {
+                                                  int32_t base = 0, int32_t from = 0) {
   const int lane = threadIdx.x & 63;
-  GroupLanes g{0, 0, 0};
-  if (base + lane < groups) {
-    g.lo = group_bound(offsets, base + lane, M);
-    g.hi = max(g.lo, group_bound(offsets, base + lane + 1, M));
+  GroupLanes g;
+  // (past the last group: no rows, from its end on)
+  g.lo = max(group_bound(offsets, min(base + lane, groups), M), from);
+  g.hi = group_bound(offsets, min(base + lane + 1, groups), M);
+  // an offset falls: the running maximum instead (rolled and out of the way: 64 rows
+  // over 32 groups 22 us, as without it; in line 23)
+  if (__builtin_expect(__ballot(g.hi < g.lo) != 0, 0)) {
+#pragma unroll 1
+    for (int s = 1; s < 64; s <<= 1) {
+      const int32_t v = __shfl_up(g.lo, s);
+      if (lane >= s) g.lo = max(g.lo, v);
+    }
+    g.hi = max(g.lo, g.hi);
   }
   g.incl = (g.hi - g.lo + tm - 1) / tm;
 #pragma unroll
@@ -88,12 +99,13 @@ __device__ __forceinline__ GroupTile group_tile_of(const GroupLanes& g, int32_t 
 
 __device__ __forceinline__ GroupTile find_group_tile(const int32_t* offsets, int32_t groups, int32_t M, int32_t tm,
                                                      int32_t u) {
-  int32_t before = 0;  // tiles of the groups already passed
+  int32_t before = 0, from = 0;  // tiles and end of the groups already passed
   for (int32_t base = 0; base < groups; base += 64) {
-    const GroupLanes g = load_groups(offsets, groups, M, tm, base);
+    const GroupLanes g = load_groups(offsets, groups, M, tm, base, from);
     const GroupTile t = group_tile_of(g, base, before, tm, u);
     if (t.group >= 0) return t;
     before += __builtin_amdgcn_readlane(g.incl, 63);
+    from = __builtin_amdgcn_readlane(g.hi, 63);
   }
   return GroupTile{-1, 0, 0, 0, 0};
 }
@@ -102,9 +114,20 @@ __device__ __forceinline__ GroupTile find_group_tile(const int32_t* offsets, int
 __device__ __forceinline__ int32_t count_group_tiles(const int32_t* offsets, int32_t groups, int32_t M, int32_t tm) {
   const int lane = threadIdx.x & 63;
   int32_t n = 0;
+  bool falls = false;
   for (int32_t g = lane; g < groups; g += 64) {
-    const int32_t lo = group_bound(offsets, g, M), hi = max(lo, group_bound(offsets, g + 1, M));
-    n += (hi - lo + tm - 1) / tm;
+    const int32_t lo = group_bound(offsets, g, M), hi = group_bound(offsets, g + 1, M);
+    falls |= hi < lo;
+    n += (max(hi, lo) - lo + tm - 1) / tm;
+  }
+  if (__ballot(falls) != 0) {
+    int32_t all = 0, from = 0;
+    for (int32_t base = 0; base < groups; base += 64) {
+      const GroupLanes g = load_groups(offsets, groups, M, tm, base, from);
+      all += __builtin_amdgcn_readlane(g.incl, 63);
+      from = __builtin_amdgcn_readlane(g.hi, 63);
+    }
+    return all;
   }
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) n += __shfl_xor(n, s);

@@ -125,7 +125,8 @@ int dist_gemm_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int
  * N).  `offsets` (device, int32, groups + 1 values) gives group g the rows
  * offsets[g] .. offsets[g + 1] - 1; any group may be empty.  Rows that no
  * group has are not written.  Offsets are read on the device and clamped
- * there to 0 .. rows and to be ascending; nothing waits for them on the host.
+ * there to 0 .. rows and to be ascending (one below an earlier one counts as
+ * that one: no row is in two groups); nothing waits for them on the host.
  *
  * A plan fixes the problem for calls with up to M rows.  Limits: 1 <= M, N
  * <= 2^31 - 1; K a multiple of 32, 32 <= K <= 2^22; 0 <= groups <= 65535. */
