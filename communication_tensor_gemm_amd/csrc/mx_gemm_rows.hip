@@ -36,7 +36,6 @@
 // E4M3 operand's lane holds elements 16 (l / 16) .. + 15 in its first four
 // registers and 64 + 16 (l / 16) .. + 15 in the last four.  The scale byte
 // that a lane passes is that of block l / 16 of its row, in both cases.
-#include "mx_shape.h"
 #include "mx_tiles.h"
 
 namespace dg {
@@ -82,8 +81,9 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemm_rows_kernel(MxGemmArgs a,
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds && kLdsA > kSums ? kLdsA : kSums];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int32_t n_tiles = (a.N + step - 1) / step;
-  const int32_t row_tile = static_cast<int32_t>(blockIdx.x) / n_tiles;
+  const int32_t n_tiles = tile_count(a.N, step);
+  const uint32_t block = blockIdx.y * kGridX + blockIdx.x;
+  const int32_t row_tile = static_cast<int32_t>(block / static_cast<uint32_t>(n_tiles));
   GroupTile t;
   int64_t b_row = 0, bias0 = 0;
   if (a.offsets) {
@@ -93,9 +93,10 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemm_rows_kernel(MxGemmArgs a,
   } else {
     t.row0 = row_tile * 16 * MB;
     t.rows = a.M - t.row0;
+    if (t.rows <= 0) return;
   }
   const int32_t rows = min(t.rows, 16 * MB);
-  const int32_t n_tile = static_cast<int32_t>(blockIdx.x) - row_tile * n_tiles;
+  const int32_t n_tile = static_cast<int32_t>(block - static_cast<uint32_t>(row_tile) * static_cast<uint32_t>(n_tiles));
   const int32_t n0 = n_tile * step, cols = min(a.N - n0, step);
   b_row += n0;
   const uint32_t b_bytes = static_cast<uint32_t>(a.K / 2), a_bytes = static_cast<uint32_t>(A8 ? a.K : a.K / 2);
@@ -283,11 +284,11 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemm_rows_kernel(MxGemmArgs a,
 
 template <int MB, int NB, bool kLds, int kWaves>
 static hipError_t rows_waves_t(const MxGemmArgs& a, hipStream_t st) {
-  const int64_t tiles = a.offsets ? most_group_tiles(a.M, a.groups, 16 * MB) : (a.M + 16 * MB - 1) / (16 * MB);
+  const int64_t tiles = a.offsets ? most_group_tiles(a.M, a.groups, 16 * MB) : tile_count(a.M, 16 * MB);
   const int step = a.offsets ? 16 * NB : rows_step(a.N, tiles, 16 * NB, a.cus);
-  const int64_t blocks = tiles * ((a.N + step - 1) / step);
+  const int64_t blocks = tiles * tile_count(a.N, step);
   if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kWaves);
+  const dim3 grid(grid_x(blocks), grid_y(blocks)), block(64 * kWaves);
   if (a.a_format == MX_E4M3) {
     if (a.out_bf16)
       hipLaunchKernelGGL((mx_gemm_rows_kernel<MB, NB, true, true, kLds, kWaves>), grid, block, 0, st, a, step);

@@ -159,13 +159,13 @@ __device__ __forceinline__ MxGemmArgs fresh_args() {
 template <typename G>
 __device__ __forceinline__ Tiles all_tiles(const MxGemmArgs& p) {
   Tiles t;
-  t.tiles_n = (p.N + G::TN - 1) / G::TN;
+  t.tiles_n = tile_count(p.N, G::TN);
   if (p.offsets) {
     t.groups = load_groups(p.offsets, p.groups, p.M, G::TM);
     t.row_tiles = p.groups <= 64 ? __builtin_amdgcn_readlane(t.groups.incl, 63)
                                  : count_group_tiles(p.offsets, p.groups, p.M, G::TM);
   } else {
-    t.row_tiles = (p.M + G::TM - 1) / G::TM;
+    t.row_tiles = tile_count(p.M, G::TM);
   }
   const int32_t T = t.row_tiles * t.tiles_n;
   const int32_t x = static_cast<int32_t>(blockIdx.x) % kXcds, each = T / kXcds, more = T % kXcds;
@@ -642,8 +642,8 @@ void mx_gemm_tile_kernel(MxGemmArgs p) {
 template <bool A8, bool kBf16, int NBM, int NBN>
 static hipError_t tile_t(const MxGemmArgs& a, hipStream_t st) {
   using G = Geo<A8, NBM, NBN>;
-  const int64_t row_tiles = a.offsets ? most_group_tiles(a.M, a.groups, G::TM) : (a.M + G::TM - 1) / G::TM;
-  const int64_t T = row_tiles * ((a.N + G::TN - 1) / G::TN);
+  const int64_t row_tiles = a.offsets ? most_group_tiles(a.M, a.groups, G::TM) : tile_count(a.M, G::TM);
+  const int64_t T = row_tiles * tile_count(a.N, G::TN);
   if (T > INT32_MAX / 2) return hipErrorInvalidConfiguration;
   const int64_t most = static_cast<int64_t>(a.cus) * G::kWgs;
   const int64_t grid = ((T < most ? T : most) + kXcds - 1) / kXcds * kXcds;

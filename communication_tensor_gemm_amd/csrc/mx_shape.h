@@ -3,8 +3,26 @@
 #pragma once
 #include <stdint.h>
 
+#if defined(__HIPCC__)
+#define DG_MX_HD __host__ __device__
+#else
+#define DG_MX_HD
+#endif
+
 namespace dg {
 namespace mx {
+
+// Tiles of `size` that n rows or columns take; n up to 2^31 - 1, whose sum with
+// a size does not fit 32 bits with a sign.
+DG_MX_HD inline int32_t tile_count(int32_t n, int32_t size) {
+  return static_cast<int32_t>((static_cast<uint32_t>(n) + static_cast<uint32_t>(size) - 1u) / static_cast<uint32_t>(size));
+}
+
+// A launch holds fewer than 2^32 threads along x: workgroups beyond kGridX go
+// on along y, as workgroup y * kGridX + x; those past the last do nothing.
+constexpr uint32_t kGridX = 1u << 21;  // of at most 1024 threads
+inline uint32_t grid_x(int64_t workgroups) { return workgroups < kGridX ? static_cast<uint32_t>(workgroups) : kGridX; }
+inline uint32_t grid_y(int64_t workgroups) { return static_cast<uint32_t>((workgroups + kGridX - 1) / kGridX); }
 
 // Columns of a workgroup of the kernel for few rows: the columns' share of what
 // makes row tiles x column tiles a multiple of the CUs, and never more than

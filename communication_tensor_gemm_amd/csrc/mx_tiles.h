@@ -2,6 +2,7 @@
 // search and the element epilogue.
 #pragma once
 #include "mx_common.h"
+#include "mx_shape.h"
 
 namespace dg {
 namespace mx {
@@ -72,7 +73,7 @@ __device__ __forceinline__ GroupLanes load_groups(const int32_t* offsets, int32_
     }
     g.hi = max(g.lo, g.hi);
   }
-  g.incl = (g.hi - g.lo + tm - 1) / tm;
+  g.incl = tile_count(g.hi - g.lo, tm);
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) {
     const int32_t v = __shfl_up(g.incl, s);
@@ -90,7 +91,7 @@ __device__ __forceinline__ GroupTile group_tile_of(const GroupLanes& g, int32_t 
   const int32_t lo = __builtin_amdgcn_readlane(g.lo, first), hi = __builtin_amdgcn_readlane(g.hi, first);
   GroupTile t;
   t.group = base + first;
-  t.tiles = (hi - lo + tm - 1) / tm;
+  t.tiles = tile_count(hi - lo, tm);
   t.index = u - (before + __builtin_amdgcn_readlane(g.incl, first) - t.tiles);
   t.row0 = lo + t.index * tm;
   t.rows = hi - t.row0;
@@ -118,7 +119,7 @@ __device__ __forceinline__ int32_t count_group_tiles(const int32_t* offsets, int
   for (int32_t g = lane; g < groups; g += 64) {
     const int32_t lo = group_bound(offsets, g, M), hi = group_bound(offsets, g + 1, M);
     falls |= hi < lo;
-    n += (max(hi, lo) - lo + tm - 1) / tm;
+    n += tile_count(max(hi, lo) - lo, tm);
   }
   if (__ballot(falls) != 0) {
     int32_t all = 0, from = 0;
