@@ -17,6 +17,7 @@
 // consecutive elements, piece c of lane t of the row at 8 (c * 64 W + t): wide
 // loads, and an MX block of 32 is four adjacent lanes.
 #include "mx_common.h"
+#include "mx_shape.h"
 
 namespace dg {
 namespace mx {
@@ -43,14 +44,14 @@ __device__ __forceinline__ float row_sum(float v, float* red, int W) {
   return s;
 }
 
-// grid: rows over workgroups of rows_per_group rows (W waves each)
+// grid: the rows over workgroups of several rows (W waves each), along x and, past kGridX, y
 template <int T, int OUT, int V, int A>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int W) {
   constexpr int kShared = A == ANY ? ANY : ALIGNED;  // what every row reads
   __shared__ float red[kMaxWaves];
   const int wave = threadIdx.x >> 6, groups = (blockDim.x >> 6) / W;
   const int t = static_cast<int>(threadIdx.x) - wave / W * W * 64, span = 64 * W;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * groups + wave / W;
+  const int64_t row = (static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x) * groups + wave / W;
   const bool live = row < a.rows;
   const int d = (a.cols + 7) / 8;
   Raw8<T> x[V];
@@ -150,7 +151,8 @@ static int row_waves(int64_t rows, int d) {
 template <int T, int OUT, int V>
 static hipError_t norm_v(const NormArgs& a, int W, int access, hipStream_t st) {
   const int groups = W >= 4 ? 1 : 4 / W;
-  const dim3 grid(static_cast<unsigned>((a.rows + groups - 1) / groups)), block(64 * W * groups);
+  const int64_t blocks = (a.rows + groups - 1) / groups;
+  const dim3 grid(grid_x(blocks), grid_y(blocks)), block(64 * W * groups);
   if (access == STREAM)
     hipLaunchKernelGGL((rms_norm_kernel<T, OUT, V, STREAM>), grid, block, 0, st, a, W);
   else if (access == ALIGNED)

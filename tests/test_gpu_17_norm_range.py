@@ -63,3 +63,35 @@ def test_gradient_of_rows_of_zeros(cols, typ):
     dg.dist_gemm_rms_norm(h, torch.ones(cols, dtype=torch_type(typ), device="cuda"), y, eps=1e-28, rstd=rstd)
     assert abs(rstd[1].item() - 1e14) <= NORM * 1e14 and not y[1].any()
     check_backward(h, h64, rstd, typ, 3)
+
+
+# more rows than a launch has threads along x for, four to a workgroup (norms per head of a long batch), up to as many as are
+# accepted
+@pytest.mark.parametrize("rows,cols,typ,out", [((1 << 26) + 13, 128, "BF16", "SAME"), ((1 << 26) + 3, 64, "BF16", "MX_E4M3"),
+                                               ((1 << 26) + 5, 512, "BF16", "E4M3"), ((1 << 31) - 1, 1, "F32", "SAME")])
+def test_many_rows_equal_their_parts(rows, cols, typ, out):
+    import torch
+    log("many rows", rows, cols, typ, out)
+    t = torch_type(typ)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.empty((rows, cols), dtype=t, device="cuda").normal_(generator=g)
+    w = torch.randn(cols, generator=g, device="cuda").to(t)
+
+    def run(x):
+        n = x.size(0)
+        y = torch.full((n, cols), 77, dtype=t if out == "SAME" else torch.uint8, device="cuda")
+        s = torch.full((n, mx.scale_pitch(cols)), 77, dtype=torch.uint8, device="cuda") if out.startswith("MX") else None
+        rstd = torch.full((n,), -1.0, device="cuda")
+        dg.dist_gemm_rms_norm(x, w, y, output=out, rstd=rstd, scales=s, scale=0.1)
+        return [v for v in (y, rstd, s) if v is not None]
+
+    whole = run(x)
+    assert bool((whole[1] > 0).all())                 # every row was reached
+    for lo in sorted({0, rows // 2, 1 << 21, 1 << 23, 1 << 24, 1 << 26, rows - 3000}):
+        lo = max(0, min(lo - 1500, rows - 3000))
+        assert all(torch.equal(p, v[lo:lo + 3000]) for p, v in zip(run(x[lo:lo + 3000]), whole))
+    x64 = f64(x[rows - 20:])
+    ref = mx.rms_norm(x64, f64(w), 1e-6)
+    assert np.all(np.abs(f64(whole[1][rows - 20:]) - ref[1]) <= NORM * ref[1])
+    if out == "SAME":
+        assert np.all(np.abs(f64(whole[0][rows - 20:]) - ref[0]) <= (OUT_STEP[typ] + 2 * NORM) * np.abs(ref[0]))
