@@ -53,6 +53,7 @@ int check_mx(const void* plain, int64_t ld, int elem, int64_t rows, int64_t cols
   MX_INVALID(!plain || !codes || !scales, "null pointer");
   MX_INVALID(!aligned(plain, elem_bytes(elem)), "the plain matrix is not aligned to its element");
   MX_INVALID(!aligned(codes, 16) || !aligned(scales, 16), "codes and scales must be 16-byte aligned");
+  MX_INVALID(codes == plain || scales == plain || codes == scales, "codes, scales and the plain matrix must not alias");
   return DIST_GEMM_OK;
 }
 
@@ -118,6 +119,10 @@ int dist_gemm_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t
              "an output that is an input needs its leading dimension");
   MX_INVALID(y == weight || h == weight || (h && h == y), "outputs must not alias the weight or each other");
   MX_INVALID(out != DIST_GEMM_NORM_SAME && (y == x || y == residual), "an 8- or 4-bit output must not alias an input");
+  const void* const others[] = {x, residual, weight, y, h};
+  for (const void* p : others)
+    MX_INVALID(p && (p == rstd || (mx && p == scales)), "rstd and scales must not alias another argument");
+  MX_INVALID(mx && rstd && rstd == scales, "rstd must not alias the scales");
   dg::NormArgs a{};
   a.x = x; a.residual = residual; a.weight = weight; a.y = y; a.h = h; a.rstd = rstd;
   a.scales = static_cast<uint8_t*>(scales);
@@ -154,6 +159,8 @@ int dist_gemm_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int
                    dweight == h || (dh && dweight == dh),
                "dweight must not alias an input, nor dx the weight or rstd");
     MX_INVALID(!workspace || !aligned(workspace, 16), "the workspace is null or misaligned");
+    const void* const others[] = {dy, h, dh, rstd, weight, dx, dweight};
+    for (const void* p : others) MX_INVALID(p == workspace, "the workspace must not alias another argument");
     MX_INVALID(workspace_bytes < dist_gemm_rms_norm_workspace(rows, cols), "the workspace is too small");
   }
   dg::NormBackwardArgs a{};
@@ -208,7 +215,8 @@ int dist_gemm_mx_run(dist_gemm_mx_plan_t P, int64_t rows, const void* A, const v
   const uint64_t es = elem_bytes(P->out_elem);
   if (!aligned(D, es) || (beta != 0.0f && !aligned(C, es)) || !aligned(bias, es) || !aligned(offsets, 4))
     return invalid("a pointer is not aligned to its element");
-  if (D == A || D == A_scales || D == B || D == B_scales || D == bias) return invalid("D must not alias an operand");
+  if (D == A || D == A_scales || D == B || D == B_scales || D == bias || D == offsets)
+    return invalid("D must not alias an operand");
   if (beta != 0.0f && C == D && ldc != ldd) return invalid("D on C needs its leading dimension");
   dg::MxGemmArgs a{};
   a.A = static_cast<const uint8_t*>(A); a.As = static_cast<const uint8_t*>(A_scales);

@@ -8,7 +8,9 @@
  * abort, and no device memory allocated by any call of this header.  Every
  * call here only launches kernels, so all of them can be captured into a HIP
  * graph.  Pointers belong to the current HIP device (a plan's: to the device
- * it was made on).
+ * it was made on).  What a call writes must not overlap its other arguments
+ * except where this header allows it; two that start at one address are
+ * refused (INVALID_ARG).
  *
  * MX tensors (OCP Microscaling Formats v1.0 element and scale types).  A
  * matrix of `rows` x `cols` values, cols a multiple of 32, is
