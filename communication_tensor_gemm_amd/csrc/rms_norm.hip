@@ -385,8 +385,9 @@ static void backward_shape(int type, int64_t rows, int64_t cols, int* W, int* gr
 template <int T, int V>
 static void backward_v(const NormBackwardArgs& a, int W, int groups, int64_t blocks, int access, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * W * groups);
+  constexpr int kStream = V <= 2 ? STREAM : ALIGNED;  // (a row that is read twice does not go past the caches)
   if (access == STREAM)
-    hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, STREAM>), grid, block, 0, st, a, W);
+    hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, kStream>), grid, block, 0, st, a, W);
   else if (access == ALIGNED)
     hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, ALIGNED>), grid, block, 0, st, a, W);
   else
@@ -405,8 +406,7 @@ static hipError_t backward_t(const NormBackwardArgs& a, hipStream_t st) {
   int64_t blocks;
   backward_shape(T, a.rows, a.cols, &W, &groups, &blocks);
   const int d = (a.cols + 7) / 8, v = (d + 64 * W - 1) / (64 * W);
-  // a row that is read twice (above 16384 columns) has to be found in the cache
-  const int access = (m & 15) != 0 || a.cols % 8 != 0 ? ANY : bytes < kLastLevelCache || v > 2 ? ALIGNED : STREAM;
+  const int access = (m & 15) != 0 || a.cols % 8 != 0 ? ANY : bytes < kLastLevelCache ? ALIGNED : STREAM;
   if (blocks == 0)
     ;  // no rows: the second kernel writes zeros
   else if (v <= 1)
