@@ -1,5 +1,5 @@
 """GPU tests of the MX products at sizes whose workgroups do not come out even,
-and with offsets that are not in order.
+with offsets that are not in order and at the ends of the scales' range.
 
 Bars as in test_gpu_13_mx_products.py, whose helpers these are."""
 import numpy as np
@@ -7,7 +7,8 @@ import pytest
 
 import communication_tensor_gemm_amd as dg
 from gpu_helpers import log
-from test_gpu_13_mx_products import check_on_gpu, dense, random_codes, up
+from oracle import codecs, mx
+from test_gpu_13_mx_products import check_on_gpu, dense, f64, random_codes, up
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,25 @@ def test_offsets_that_fall(rows, N, K, offsets, a_format):
         if at[e + 1] > at[e]:
             check_on_gpu(D[at[e]:at[e + 1]], a[at[e]:at[e + 1]], b[e * N:(e + 1) * N], "BF16")
     assert bool((D[:at[0]] == -5.0).all()) and bool((D[at[-1]:] == -5.0).all())
+
+
+@pytest.mark.parametrize("a_format", ["E2M1", "E4M3"])
+@pytest.mark.parametrize("M,N", [(16, 255), (64, 255), (1100, 1100), (2304, 1100)])
+def test_scales_over_their_whole_range(M, N, a_format):
+    """One product per element, 2^(a - 127) 2^(b - 127) for all scale bytes a and b but NaN: exact down to the smallest
+    subnormal, zero below, infinite above."""
+    import torch
+    log("all scales", M, N, a_format)
+    K = 512
+    a, b = np.zeros((M, K)), np.zeros((N, K))
+    a[:, 5], b[:, 5] = 1.0, 1.0
+    A = mx.pack(mx.f64_to_e2m1(a)) if a_format == "E2M1" else codecs.f64_to_e4m3(a)
+    As, Bs = np.zeros((M, mx.scale_pitch(K)), dtype=np.uint8), np.zeros((N, mx.scale_pitch(K)), dtype=np.uint8)
+    As[:, 0], Bs[:, 0] = np.arange(M) * 7 % 255, np.arange(N) % 255
+    D = torch.empty((M, N), device="cuda")
+    with dg.MxPlan(M, N, K, a_format=a_format, out_dtype="F32") as p:
+        p.run(up(A), up(As), up(mx.pack(mx.f64_to_e2m1(b))), up(Bs), D)
+    e = As[:, :1].astype(int) + Bs[:, 0].astype(int)[None] - 254
+    want = np.where(e > 127, np.inf, np.where(e < -149, 0.0, np.ldexp(1.0, np.clip(e, -149, 127))))
+    # halfway between zero and the smallest subnormal goes to zero (even)
+    assert np.array_equal(f64(D), want)
