@@ -27,9 +27,11 @@
 // than 832 times 16, of which some CUs would have four and some three (27.2 ->
 // 24.0 us).
 //
-// At 1 x 13312 x 16384 (116 MB) it reads 4.9 TB/s, launch and the latency of
-// the first loads included (5.4 with E2M1 rows); a plain read of such a tensor
-// reaches 6.2.
+// At 1 x 13312 x 16384 (116 MB) it reads 5.2 TB/s, launch and the latency of
+// the first loads included (5.6 with E2M1 rows); a plain read of such a tensor
+// reaches 6.2.  More rows of that width, whose A is read again by every
+// workgroup (E4M3 / E2M1, us): 2 23, 4 and 8 26, 16 29 / 26, 32 38 / 30, 64
+// 54 / 42.
 //
 // Operand layout of the MFMA (k within its 128): lane l has row l % 16 of its
 // operand; an E2M1 operand's lane holds the 32 elements of block l / 16; an
@@ -305,17 +307,20 @@ static hipError_t rows_waves_t(const MxGemmArgs& a, hipStream_t st) {
 
 // Eight waves to a workgroup; four where there are many workgroups of few
 // chunks each, so that more of them are under way at once (by group, 64 rows, 32
-// x 2048 x 4096, E4M3: 21.6 us, with eight 25.5; dense at 8192 x 8192 and one row
-// eight take 9.5 us, four 11.3).
+// x 2048 x K, four / eight, us: K = 1024 E2M1 15.6 / 18.1, E4M3 16.4 / 24.2;
+// 4096 24.0 / 26.4, 23.6 / 25.8; 8192 39.0 / 38.8, 42.5 / 42.0; dense at 8192 x
+// 8192 and one row eight take 9.5 us, four 11.3).
 template <int MB, int NB, bool kLds>
 static hipError_t rows_lds_t(const MxGemmArgs& a, hipStream_t st) {
   return a.offsets && a.K <= 8 * kChunk ? rows_waves_t<MB, NB, kLds, 4>(a, st) : rows_waves_t<MB, NB, kLds, 8>(a, st);
 }
 
 // Rows that fit into LDS leave a wave little else to load than B: 16 columns,
-// in two chunks ahead (1 x 13312 x 16384, E4M3: 23.0 us, with 32 columns 26.9).
-// More of them: 32 columns, for half the reads of A (16 rows: 28.8 us, with 16
-// columns 35.5; 64 rows: 54 and 82).
+// in two chunks ahead (1 x 13312 x 16384: E4M3 23.7 us, with 32 columns 26.8,
+// E2M1 21.9 and 24.7; 1 x 8192 x 3584 6.7 and 7.1, 6.4 and 6.7).  More of them: 32
+// columns, for half the reads of A (16 rows: 28.8 us, with 16 columns 35.5; 64
+// rows: 54 and 82).  A short K is not told apart, and there the first form loses
+// (4 x 8192 x 4096 7.3 against 7.2, 16 x 8192 x 1024 5.9 against 4.5).
 template <int MB>
 static hipError_t rows_t(const MxGemmArgs& a, hipStream_t st) {
   // of a group: as many rows as a tile can have
@@ -326,19 +331,27 @@ static hipError_t rows_t(const MxGemmArgs& a, hipStream_t st) {
 
 }  // namespace mx
 
-// Few rows stream the weights; from 65 rows on (of a group, on average), tiles
-// (128 x 13312 x 16384, E4M3: 58 us against 100 in two passes of 64 rows).
+// (Times in us, E2M1 then E4M3, operands from memory.)
+//
+// Few rows stream the weights; from 65 rows on (of a group, on average), tiles,
+// where two passes of 64 rows read all weights twice (tiles / two passes: 65 x
+// 13312 x 16384 56 / 64, 64 / 90; 128 rows 60 / 71, 74 / 102; 65 x 8192 x 3584 13.2
+// / 13.5, 17.1 / 19.5).  For groups that bound is too high: 16 x 4096 x 4096 takes
+// 45 / 55 here with 512 rows (35 / 41 on tiles of 128) and 71 / 134 with 1024 (50 /
+// 56), whether evenly spread or half of them in one group.
 //
 // Few tiles would leave most CUs idle: then 32 rows at a time here, K split over
-// a workgroup's waves (E4M3, this / tiles of 128: 126 x 113 x 15168 12 / 49 us,
-// 128 x 512 x 1024 6.2 / 7.7, 512 x 1024 x 3584 10.5 / 16.6; 512 x 2048, 64
-// tiles: K = 3584 18.2 / 16.9, 15168 50 / 62).
+// a workgroup's waves (this / tiles of 128: 126 x 113 x 15168 11 / 51, 14 / 62;
+// 128 x 512 x 1024 4.8 / 6.6, 5.3 / 8.0; 512 x 1024 x 3584 8.4 / 12.6, 12.4 / 17.3;
+// 512 x 2048, 64 tiles: K = 3584 14.5 / 13.8, 20.6 / 17.7, K = 15168 36 / 50, 53 / 63).
 //
 // Tiles of 256 x 256 read the operands half as often, tiles of 128 x 128 leave
 // fewer CUs idle in the last round.  A round of the larger ones takes as long
-// as three of the smaller ones with one per CU (M x 8192 x 4096, E4M3, larger /
-// smaller: M = 1024 49 / 38 us, 1536 53 / 55, 2048 62 / 73, 2304 95 / 87, 4096
-// 117 / 142).  A group's last tile is taken as half full.
+// as three of the smaller ones with one per CU (M x 8192 x 4096, larger /
+// smaller: M = 1024 34 / 27, 50 / 37; 1536 37 / 39, 52 / 52; 2048 41 / 47, 58 / 69;
+// 2304 63 / 57, 95 / 79; 4096 75 / 93, 109 / 134; 1024 x 13312 x 16384 122 / 168,
+// 177 / 234; 2048 x 4096 x 1024 15.6 / 13.1, 20 / 16).  A group's last tile is taken
+// as half full.
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t st) {
   if (a.M == 0) return hipSuccess;
   const int64_t rows = a.offsets ? a.M / a.groups : a.M;

@@ -32,15 +32,28 @@
 // do not cover its loads' latency and its other instructions (0.7 us per slab,
 // deeper stages or not).  With a long K, two groups of four waves then compute
 // half of a tile's K each, with stages of their own, and the second group's
-// sums go to the first through LDS at the end: 128 x 13312 x 16384 E2M1 48.4 ->
-// 42.6 us.  That end costs 1.5 us, so for K up to 4096 one group is as fast or
-// faster (256 x 8192 x 3584: 12.6 us, with two 14.1).
+// sums go to the first through LDS at the end: 128 x 13312 x 16384 E2M1 69 -> 60
+// us (E4M3 72 -> 70), 256 x 8192 x 8192 28 -> 25 (36 -> 34).  That end costs 1.5
+// us, so for K up to 4096 one group is as fast or faster (256 x 8192 x 3584: 14.9
+// us, with two 16.1; E4M3 19.1 and 20.7; at 200 x 8192 x 4096 two gain 3%, at 512 x
+// 4096 x 4608 they lose 5% of E4M3).
 //
 // Rates.  16384 x 13312 x 16384 E2M1: 1575 .. 1620 us, 4.4 .. 4.5 PFLOP/s, 70%
 // of what MFMAs alone reach on random data (6.5): the MFMA pipe is busy 65% of
-// the cycles at 1.8 GHz (power), waits take 24%.  E4M3: 2.9 PFLOP/s (MFMAs alone
-// 4.0).  By group, 8192 rows x 16 x 4096 x 4096 E4M3: 148 us; a round of tiles
-// takes 47 and the last one, here half empty, as long as the others.
+// the cycles at 1.8 GHz (power), waits take 24%.  E4M3: 2510 us, 2.85 PFLOP/s
+// (MFMAs alone 4.0).  By group, 8192 rows x 16 x 4096 x 4096 E4M3: 148 us (E2M1
+// 108); a round of tiles takes 47 and the last one, here half empty, as long as
+// the others.  What is not whole bf16 columns without C goes four columns of a row
+// at a time, C and bias by single elements: 4096 x 8192 x 4096 E2M1 76 us, with a
+// bias 90, into fp32 109, with C 162 (171).
+//
+// Precision.  The matrix cores add the products of eight consecutive elements
+// to 2^-13 of the largest one's power of two and cut off what lies below (measured
+// on both MFMAs of these products); from there on sums are fp32.  E2M1 products,
+// from 1/4 to 36, are all within that: exact.  E4M3 elements spread over 2^17, and
+// their products' sums are off by 1.7e-5 of the result's rms with normal data, for
+// any K, without a bias to one side (an fp32 product: 3e-8).  It is the price
+// of the 8-bit rate, a hundredth of what rounding D to bf16 costs.
 //
 // Operand layout (see mx_gemm_rows.hip for the other MFMA's): lane l has row
 // l % 32 and, with h = l / 32, an E2M1 block of 32 elements, or of E4M3

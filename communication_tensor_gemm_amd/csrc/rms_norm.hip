@@ -11,7 +11,11 @@
 // us, 6.1 TB/s (a copy of the size: 6.2); 4 x 16384 into MX E4M3: 5 us, the
 // latency of a load, two sums over 16 waves and a store; the gradient of 8192 x
 // 8192 bf16 with dh: 95 us, 5.6 TB/s (its second kernel 4.4 of them), of 1021 x
-// 5123 fp32 18 us, two launches.
+// 5123 fp32 18 us, two launches.  Rows of few columns are bound by their waves: a
+// row has one of its own, 262144 x 128 bf16 takes 71 us, 1.9 TB/s, with 16 of 64
+// lanes at work (256 columns 74 us), its gradient 74.
+//
+// (The sum of squares is fp32: a row past 1.8e19 / sqrt(cols) overflows it.)
 //
 // A row belongs to W waves (W = 1 .. 16), each lane holding V pieces of eight
 // consecutive elements, piece c of lane t of the row at 8 (c * 64 W + t): wide
@@ -200,7 +204,10 @@ static hipError_t norm_out(int out, const NormArgs& a, hipStream_t st) {
 // of up to 8192 and 16384 columns) the next row's loads are in flight while
 // the current row's sum crosses the waves; longer rows have no registers for
 // that, and above 16384 columns the row itself is read again (from the L2)
-// after its sum.
+// after its sum.  There a lane's 32 column sums and the pieces do not fit 128
+// registers either, and 164 to 276 bytes per lane go to scratch: 4096 x 32768 bf16
+// with dh takes 452 us, 2.4 TB/s, 8192 x 16384 192 us, 5.6 TB/s (two pieces of
+// bf16 keep 20 bytes of scratch, none of them in the loop over the rows).
 template <int T, int V, int A>
 __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormBackwardArgs a, int W) {
   constexpr int kShared = A == ANY ? ANY : ALIGNED;
