@@ -45,3 +45,17 @@ from ._mx import (  # noqa: F401
     dist_gemm_rms_norm_backward,
     dist_gemm_rms_norm_workspace,
 )
+from ._f8 import (  # noqa: F401
+    F8_C_FUNCTIONS,
+    LAYER_NORM_OUTPUTS,
+    dist_gemm_f8_dequantize,
+    dist_gemm_f8_pitch,
+    dist_gemm_f8_product,
+    dist_gemm_f8_product_workspace,
+    dist_gemm_f8_quantize,
+    dist_gemm_f8_scale_pitch,
+    dist_gemm_f8_transpose,
+    dist_gemm_layer_norm,
+    dist_gemm_layer_norm_backward,
+    dist_gemm_layer_norm_workspace,
+)

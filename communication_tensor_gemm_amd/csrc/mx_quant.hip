@@ -9,23 +9,10 @@
 // 13312 bf16 to E4M3: 54 us, 6.1 TB/s (a copy: 6.2); 777 x 3584 to E2M1 and back:
 // 3.7 and 4.2 us, a launch's latency more than its bytes (2.3 us for both).
 #include "mx_common.h"
+#include "piece_rows.h"
 
 namespace dg {
 namespace mx {
-
-constexpr int kThreads = 256, kPieces = 4;
-constexpr int kSegment = kThreads * kPieces;  // eight-element pieces of one workgroup
-
-// Pieces are numbered through all rows (d to a row), a workgroup takes
-// kSegment of them, so every lane has work whatever the row's length.  n / d
-// for n below 2^31 is one product and a shift: with 2^(s-1) < d <= 2^s and m =
-// floor(2^(31+s) / d) + 1, it is floor(n m / 2^(31+s)).
-struct Rows {
-  uint32_t d, m, shift;  // shift = s - 1
-  uint32_t pieces;       // of a chunk of rows (one per blockIdx.y), below 2^31
-  int64_t rows;          // of a chunk
-};
-__device__ __forceinline__ uint32_t row_of(const Rows& r, uint32_t n) { return __umulhi(n, r.m) >> r.shift; }
 
 template <int T, int FMT, int A>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a, Rows rows) {
@@ -127,20 +114,6 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(DequantizeArgs a, 
     out.set(v);
     out.template store<A>(a.y, row[c] * a.ldy + 8 * static_cast<int64_t>(col[c]), 8);
   }
-}
-
-static Rows split_rows(int64_t rows, int64_t cols, dim3* grid) {
-  Rows r;
-  r.d = static_cast<uint32_t>(cols / 8);
-  uint32_t s = 0;
-  while ((uint64_t{1} << s) < r.d) ++s;
-  r.shift = s - 1;  // d is at least 4
-  r.m = static_cast<uint32_t>((uint64_t{1} << (31 + s)) / r.d + 1);
-  const int64_t most = ((int64_t{1} << 31) - kSegment) / r.d;  // rows whose pieces stay below 2^31
-  r.rows = rows < most ? rows : most;
-  r.pieces = static_cast<uint32_t>(r.rows * r.d);
-  *grid = dim3((r.pieces + kSegment - 1) / kSegment, static_cast<unsigned>((rows + r.rows - 1) / r.rows));
-  return r;
 }
 
 template <int T, int FMT>

@@ -1,0 +1,68 @@
+"""The F8 product kernels count their own loads and stores in s_waitcnt vmcnt
+immediates, as the MX product kernels do (test_mx_waits_asm.py says how and
+has the checks); here the F8 kernels' listings.
+
+CPU only (hipcc cross-compiles); skipped where hipcc is missing."""
+import os
+import re
+import shutil
+from concurrent.futures import ThreadPoolExecutor
+
+import pytest
+
+from test_epilogue_asm import _build_module, _device_asm, _kernels
+from test_mx_waits_asm import events, rows_ok, tile_ok
+
+pytestmark = pytest.mark.skipif(shutil.which("hipcc") is None and not os.path.exists("/opt/rocm/bin/hipcc"),
+                                reason="hipcc not available")
+
+
+@pytest.fixture(scope="module")
+def listings(tmp_path_factory):
+    B, tmp = _build_module(), tmp_path_factory.mktemp("asm")
+    srcs = ["f8_gemm_rows.hip", "f8_gemm_tile.hip"]
+    with ThreadPoolExecutor(2) as ex:
+        return [_kernels(t) for t in ex.map(lambda s: _device_asm(B, s, str(tmp / (s + ".s"))), srcs)]
+
+
+def geometry(bf16, nb):
+    """128 bytes per row of both operands in a slab, two stages; a chunk of 16 scale bytes per row."""
+    return dict(loads=2 * (64 * nb * 128 // 4096), stages=2, scales=2 * 64 * nb * 16 // 4096, stores=2 * nb * nb if bf16 else 0)
+
+
+def test_few_rows(listings):
+    checked = 0
+    for name, body in listings[0].items():
+        m = re.search(r"f8_gemm_rows_kernelILi(\d)ELi(\d)ELb(\d)ELb1E", name)
+        if not m:
+            continue
+        assert m.group(2) == "1", name      # the wait counts one column block
+        assert rows_ok(events(body)), (name, events(body)[:200])
+        checked += 1
+    assert checked == 3 * 2                  # row blocks, outputs
+
+
+def test_tiles(listings):
+    checked = 0
+    for name, body in listings[1].items():
+        m = re.search(r"f8_gemm_tile_kernelILb(\d)ELi(\d)ELi(\d)ELi(\d)E", name)
+        if not m:
+            continue
+        assert m.group(2) == m.group(3), name
+        g = geometry(m.group(1) == "1", int(m.group(2)))
+        ev = events(body)
+        if int(m.group(4)) == 1:
+            # K is whole slabs: no branch stands between the scales' loads and the first stage's
+            ev.insert([i for i, e in enumerate(ev) if e == "L"][g["scales"] - 1] + 1, "|")
+        assert tile_ok(ev, **g), (name, g)
+        for what in "LS":                    # and every one of them counts
+            for i in [k for k, e in enumerate(ev) if e == what]:
+                assert not tile_ok(ev[:i] + ev[i + 1:], **g), (name, i)
+        checked += 1
+    assert checked == 2 * 3                  # outputs, tile sizes and split K
+
+
+def test_no_kernel_reads_spilled_registers(listings):
+    """A spill's loads would count among those that the waits count."""
+    for body in [b for l in listings for b in l.values()]:
+        assert not any(line.split() and line.split()[0].startswith("scratch_") for line in body)
