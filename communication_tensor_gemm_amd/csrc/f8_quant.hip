@@ -75,51 +75,81 @@ __global__ __launch_bounds__(kThreads) void f8_rows_kernel(F8QuantizeArgs a, Row
   }
 }
 
-// Eight consecutive elements of a row of the square, as loaded.
+// Eight consecutive elements of a row of the square, as loaded, from `at` elements (bytes, of an F8 tensor) on.
 template <int SRC>
 struct Piece {
   Raw8<SRC> raw;
   template <int A>
-  __device__ __forceinline__ void load(const F8QuantizeArgs& a, int64_t row, int64_t col, int64_t) {
-    raw.template load<A>(a.x, row * a.ldx + col, static_cast<int>(min(a.cols - col, int64_t{8})));
+  __device__ __forceinline__ void load(const F8QuantizeArgs& a, int64_t at, int64_t, int64_t col) {
+    raw.template load<A>(a.x, at, static_cast<int>(min(a.cols - col, int64_t{8})));
   }
   __device__ __forceinline__ void zero() { raw.zero(); }
+  // elements 4 h .. + 3 of the eight
+  __device__ __forceinline__ void four(int h, float (&v)[4]) const {
+    float f[8];
+    raw.get(f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = f[4 * h + j];
+  }
+  __device__ __forceinline__ bool none() const { return false; }
 };
 template <>
 struct Piece<PT_F8> {
   u32x2 w;
   uint32_t byte;
   template <int A>
-  __device__ __forceinline__ void load(const F8QuantizeArgs& a, int64_t row, int64_t col, int64_t spitch) {
-    w = load_wide<A>(reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.x) + row * a.ldx + col));
-    byte = a.x_scales[row * spitch + col / kF8Block];
-    // what lies past the columns is no value (its column is not written)
+  __device__ __forceinline__ void load(const F8QuantizeArgs& a, int64_t at, int64_t scale_at, int64_t) {
+    // (codes past the columns are no values: their column is not written)
+    w = load_wide<A>(reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.x) + at));
+    byte = a.x_scales[scale_at];
   }
   __device__ __forceinline__ void zero() {
     w = u32x2{0, 0};
     byte = 0;
   }
+  __device__ __forceinline__ void four(int h, float (&v)[4]) const {
+    const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], block_factor(byte), false);
+    const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], block_factor(byte), true);
+    v[0] = lo[0]; v[1] = lo[1]; v[2] = hi[0]; v[3] = hi[1];
+  }
+  __device__ __forceinline__ bool none() const { return byte == 255u; }  // the block is NaN
 };
 
-// grid: the squares, those of one band of rows after one another
+// The squares' order: workgroup b runs on XCD b mod 8 and takes place b / 8 of
+// that XCD's contiguous share; the order goes down kBands bands of rows, then
+// one square to the right, so that the bytes of a line of scales (one per square,
+// of either tensor) meet in one L2.
+constexpr uint32_t kXcds = 8, kBands = 16;
+struct Squares {
+  uint32_t bands, across;
+};
+__device__ __forceinline__ bool square_of(const Squares& q, uint32_t block, uint32_t& band, uint32_t& kb) {
+  const uint32_t n = q.bands * q.across, x = block % kXcds, i = block / kXcds, each = n / kXcds, more = n % kXcds;
+  if (i >= each + (x < more ? 1u : 0u)) return false;
+  const uint32_t w = x * each + min(x, more) + i, group = w / (kBands * q.across), in = w - group * kBands * q.across;
+  const uint32_t high = min(kBands, q.bands - group * kBands);
+  band = group * kBands + in % high;
+  kb = in / high;
+  return true;
+}
+
 template <int SRC, int A>
-__global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, uint32_t across) {
+__global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, Squares squares) {
   __shared__ __attribute__((aligned(16))) uint32_t most[4][128];
   __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 128];
-  const uint32_t square = blockIdx.y * kGridX + blockIdx.x, band = square / across, kb = square - band * across;
+  uint32_t band, kb;
+  if (!square_of(squares, blockIdx.y * kGridX + blockIdx.x, band, kb)) return;
   const int64_t row0 = static_cast<int64_t>(band) * 128, col0 = static_cast<int64_t>(kb) * 128;
-  if (row0 >= a.rows) return;
   const int t = threadIdx.x, c8 = t & 15, rg = t >> 4, wave = t >> 6;
-  const int64_t spitch = f8_scale_pitch(a.cols), col = col0 + 8 * c8;
+  const int64_t spitch = f8_scale_pitch(a.cols), col = col0 + 8 * c8, row_at = row0 + 8 * rg;
   Piece<SRC> in[8];
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
-    const int64_t row = row0 + 8 * rg + p;
     in[p].zero();
-    if (row < a.rows && col < a.cols) in[p].template load<A>(a, row, col, spitch);
+    if (row_at + p < a.rows && col < a.cols)
+      in[p].template load<A>(a, row_at * a.ldx + col + p * a.ldx, (row_at + p) * spitch + kb, col);
   }
   // magnitudes: of the thread's rows (rm) and columns (cm)
-  float v[SRC == PT_BF16 ? 1 : 8][8];
   uint32_t rm[8], cm[8];
   if constexpr (SRC == PT_BF16) {
     uint32_t pair[4] = {0, 0, 0, 0};
@@ -144,25 +174,27 @@ __global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, u
     for (int j = 0; j < 8; ++j) cm[j] = 0;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      if constexpr (SRC == PT_F8)
-        unpack8(in[p].w, block_factor(in[p].byte), v[p]);
-      else
-        in[p].raw.get(v[p]);
       rm[p] = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t m = magnitude(v[p][j]);
-        if constexpr (SRC == PT_F8) m = in[p].byte == 255u ? 0x7f800000u : m;
-        rm[p] = max(rm[p], m);
-        cm[j] = max(cm[j], m);
+      for (int h = 0; h < 2; ++h) {
+        float v[4];
+        in[p].four(h, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t m = in[p].none() ? 0x7f800000u : magnitude(v[j]);
+          rm[p] = max(rm[p], m);
+          cm[4 * h + j] = max(cm[4 * h + j], m);
+        }
       }
     }
   }
   // columns: over the wave's four groups of rows, then over the waves
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    cm[j] = max(cm[j], static_cast<uint32_t>(__shfl_xor(static_cast<int>(cm[j]), 16)));
-    cm[j] = max(cm[j], static_cast<uint32_t>(__shfl_xor(static_cast<int>(cm[j]), 32)));
+    const auto x = __builtin_amdgcn_permlane16_swap(cm[j], cm[j], false, false);
+    const uint32_t m = max(x[0], x[1]);
+    const auto y = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    cm[j] = max(y[0], y[1]);
   }
   if ((t & 63) < 16) {
     *reinterpret_cast<u32x4*>(&most[wave][8 * c8]) = u32x4{cm[0], cm[1], cm[2], cm[3]};
@@ -182,16 +214,19 @@ __global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, u
       const int64_t pitch = f8_pitch(a.cols), blocks = pitch / kF8Block;
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
-        const int64_t row = row0 + 8 * rg + p;
+        const int64_t row = row_at + p;
         const uint32_t byte = block_byte(a.square ? all : row16_max(rm[p]));
         if (row >= a.rows) continue;
         u32x2 w;
-        if constexpr (SRC == PT_BF16)
+        if constexpr (SRC == PT_BF16) {
           w = pack8_bf16(in[p].raw.w, block_factor(byte));
-        else
-          w = pack8(v[p], block_factor(byte));
+        } else {
+          float v[8];
+          in[p].raw.get(v);
+          w = pack8(v, block_factor(byte));
+        }
         if (byte == 255u) w = u32x2{0, 0};
-        store_wide<A>(reinterpret_cast<u32x2*>(a.codes + row * pitch + col), w);
+        store_wide<A>(reinterpret_cast<u32x2*>(a.codes + row_at * pitch + col + p * pitch), w);
         if (c8 == 0) a.scales[row * spitch + kb] = static_cast<uint8_t>(byte);
         if (kb == blocks - 1 && c8 < spitch - blocks) a.scales[row * spitch + blocks + c8] = 0;
       }
@@ -200,24 +235,23 @@ __global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, u
   if (!a.codes_t) return;
   const int64_t pitch_t = f8_pitch(a.rows), spitch_t = f8_scale_pitch(a.rows), blocks_t = pitch_t / kF8Block;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t byte = block_byte(a.square ? all : cm[j]);
-    const float factor = block_factor(byte);
-    float r[8];
+  for (int h = 0; h < 2; ++h) {
+    float v[8][4];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      if constexpr (SRC == PT_BF16)
-        r[p] = j & 1 ? bf16_hi(in[p].raw.w[j / 2]) : bf16_lo(in[p].raw.w[j / 2]);
-      else
-        r[p] = v[p][j];
+    for (int p = 0; p < 8; ++p) in[p].four(h, v[p]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 4 * h + i;
+      const uint32_t byte = block_byte(a.square ? all : cm[j]);
+      const float r[8] = {v[0][i], v[1][i], v[2][i], v[3][i], v[4][i], v[5][i], v[6][i], v[7][i]};
+      u32x2 w = pack8(r, block_factor(byte));
+      if (byte == 255u) w = u32x2{0, 0};
+      // column 8 c8 + j, its rows' pieces of 8 permuted by c8: the 16 columns of a write are on banks of their own
+      *reinterpret_cast<u32x2*>(turned + (8 * c8 + j) * 128 + 8 * (rg ^ c8)) = w;
+      if (rg == 0 && col + j < a.cols) a.scales_t[(col + j) * spitch_t + band] = static_cast<uint8_t>(byte);
+      if (band == blocks_t - 1 && rg < spitch_t - blocks_t && col + j < a.cols)
+        a.scales_t[(col + j) * spitch_t + blocks_t + rg] = 0;
     }
-    u32x2 w = pack8(r, factor);
-    if (byte == 255u) w = u32x2{0, 0};
-    // column 8 c8 + j, its rows' pieces of 8 permuted by c8: the 16 columns of a write are on banks of their own
-    *reinterpret_cast<u32x2*>(turned + (8 * c8 + j) * 128 + 8 * (rg ^ c8)) = w;
-    if (rg == 0 && col + j < a.cols) a.scales_t[(col + j) * spitch_t + band] = static_cast<uint8_t>(byte);
-    if (band == blocks_t - 1 && rg < spitch_t - blocks_t && col + j < a.cols)
-      a.scales_t[(col + j) * spitch_t + blocks_t + rg] = 0;
   }
   __syncthreads();
 #pragma unroll
@@ -289,9 +323,9 @@ static void rows_t(const F8QuantizeArgs& a, int access, hipStream_t st) {
 
 template <int SRC>
 static void square_t(const F8QuantizeArgs& a, int access, hipStream_t st) {
-  const int64_t across = f8_blocks(a.cols), squares = f8_blocks(a.rows) * across;
+  const Squares n{static_cast<uint32_t>(f8_blocks(a.rows)), static_cast<uint32_t>(f8_blocks(a.cols))};
+  const int64_t squares = (static_cast<int64_t>(n.bands) * n.across + kXcds - 1) / kXcds * kXcds;
   const dim3 grid(grid_x(squares), grid_y(squares));
-  const uint32_t n = static_cast<uint32_t>(across);
   if (access == STREAM)
     hipLaunchKernelGGL((f8_square_kernel<SRC, STREAM>), grid, dim3(kThreads), 0, st, a, n);
   else if (access == ALIGNED || SRC == PT_F8)

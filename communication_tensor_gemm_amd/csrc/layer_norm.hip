@@ -61,7 +61,8 @@ template <int T, int OUT, int V, int A>
 __global__ __launch_bounds__(1024) void layer_norm_kernel(LayerNormArgs a, int W) {
   constexpr int kShared = A == ANY ? ANY : ALIGNED;  // what every row reads
   __shared__ f32x2 parts[kMaxWaves];
-  const int wave = threadIdx.x >> 6, groups = (blockDim.x >> 6) / W, part = wave % W;
+  // (a wave's row is one: kept in scalar registers, with its addresses)
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), groups = (blockDim.x >> 6) / W, part = wave % W;
   const int t = part * 64 + (threadIdx.x & 63), span = 64 * W;
   const int64_t row = (static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x) * groups + wave / W;
   const bool live = row < a.rows;
@@ -262,17 +263,16 @@ static void norm_out(int out, const LayerNormArgs& a, hipStream_t st) {
 // the columns' sums: there the first kernel leaves them to a kernel that walks
 // down the columns.
 
-// Eight elements of a row's dy, n (or h) and dh, as loaded.
+// Eight elements of a row's dy and n (or h), as loaded.
 template <int T, bool KEPT>
-struct Triple {
-  Raw8<T> dy, dh, h;
+struct Pair {
+  Raw8<T> dy, h;
   u32x2 code;
   uint32_t byte;
   template <int A>
   __device__ __forceinline__ void load(const LayerNormBackwardArgs& a, int64_t row, int i, bool in) {
     const int n = a.cols - 8 * i;
     dy.zero();
-    dh.zero();
     if constexpr (KEPT) {
       code = u32x2{0, 0};
       byte = 0;
@@ -287,7 +287,6 @@ struct Triple {
     } else {
       h.template load<A>(a.h, row * a.ldh + 8 * i, n);
     }
-    if (a.dh) dh.template load<A>(a.dh, row * a.lddh + 8 * i, n);
   }
   // g = dy w (w of zeros past the columns) and n
   __device__ __forceinline__ void get(float mean, float s, float (&y)[8], float (&n)[8]) const {
@@ -312,7 +311,8 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBack
   constexpr bool kSums = V <= 2, kAhead = V == 1 || (V == 2 && T == PT_BF16);
   constexpr int N = kAhead ? V : 1;
   __shared__ f32x2 red[2][kMaxWaves];
-  const int wave = threadIdx.x >> 6, groups = (blockDim.x >> 6) / W, part = wave % W;
+  // (a wave's row is one: kept in scalar registers, with its addresses)
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), groups = (blockDim.x >> 6) / W, part = wave % W;
   const int t = part * 64 + (threadIdx.x & 63), span = 64 * W;
   const int d = (a.cols + 7) / 8;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
@@ -335,9 +335,15 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBack
   // all groups of the workgroup make the same number of turns (they share the barrier)
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + wave / W;
   const int64_t turns = (a.rows - static_cast<int64_t>(blockIdx.x) * groups + step - 1) / step;
-  Triple<T, KEPT> in[V], ahead[N];
+  Pair<T, KEPT> in[V], ahead[N];
+  Raw8<T> dh[kSums ? V : 1];
+  auto fetch_dh = [&](int64_t r, int c, Raw8<T>& e) {
+    const int i = c * span + t;
+    e.zero();
+    if (a.dh && r < a.rows && i < d) e.template load<A>(a.dh, r * a.lddh + 8 * i, a.cols - 8 * i);
+  };
   float s = 0.0f, s1 = 0.0f, mu = 0.0f, mu1 = 0.0f;
-  auto fetch = [&](int64_t r, int c, Triple<T, KEPT>& p) {
+  auto fetch = [&](int64_t r, int c, Pair<T, KEPT>& p) {
     const int i = c * span + t;
     p.template load<A>(a, r, i, r < a.rows && i < d);
   };
@@ -351,6 +357,11 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBack
     for (int c = 0; c < V; ++c) fetch(row, c, ahead[c]);
   }
   for (int64_t k = 0; k < turns; ++k) {
+    // (dh is used behind the sums: asked for now, it needs no registers a row ahead)
+    if constexpr (kSums) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) fetch_dh(row, c, dh[c]);
+    }
     if constexpr (kAhead) {
       s = s1;
       mu = mu1;
@@ -419,7 +430,8 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBack
         weight(c, r);
         r.get(w);
       }
-      in[c].dh.get(e);
+      if constexpr (!kSums) fetch_dh(row, c, dh[0]);
+      dh[kSums ? c : 0].get(e);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = __builtin_fmaf(s, __builtin_fmaf(n[j], -sgn, __builtin_fmaf(y[j], w[j], -sg)), e[j]);
       Raw8<T> out;
@@ -471,12 +483,10 @@ __global__ __launch_bounds__(256) void layer_norm_columns_kernel(LayerNormBackwa
   float dw[8], db[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) dw[j] = db[j] = 0.0f;
-  LayerNormBackwardArgs only = a;
-  only.dh = nullptr;
 #pragma unroll 4
   for (int64_t row = static_cast<int64_t>(blockIdx.y) * 4 + wave; row < a.rows; row += static_cast<int64_t>(gridDim.y) * 4) {
-    Triple<T, KEPT> p;
-    p.template load<A>(only, row, i, in);
+    Pair<T, KEPT> p;
+    p.template load<A>(a, row, i, in);
     float y[8], n[8];
     p.get(KEPT ? 0.0f : a.mean[row], a.rstd[row], y, n);
 #pragma unroll
