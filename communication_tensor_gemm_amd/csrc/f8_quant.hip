@@ -75,15 +75,10 @@ __global__ __launch_bounds__(kThreads) void f8_rows_kernel(F8QuantizeArgs a, Row
   }
 }
 
-// Eight consecutive elements of a row of the square, as loaded, from `at` elements (bytes, of an F8 tensor) on.
+// Eight consecutive elements of a row of the square, as loaded.
 template <int SRC>
 struct Piece {
   Raw8<SRC> raw;
-  template <int A>
-  __device__ __forceinline__ void load(const F8QuantizeArgs& a, int64_t at, int64_t, int64_t col) {
-    raw.template load<A>(a.x, at, static_cast<int>(min(a.cols - col, int64_t{8})));
-  }
-  __device__ __forceinline__ void zero() { raw.zero(); }
   // elements 4 h .. + 3 of the eight
   __device__ __forceinline__ void four(int h, float (&v)[4]) const {
     float f[8];
@@ -91,29 +86,23 @@ struct Piece {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = f[4 * h + j];
   }
-  __device__ __forceinline__ bool none() const { return false; }
 };
 template <>
 struct Piece<PT_F8> {
   u32x2 w;
   uint32_t byte;
-  template <int A>
-  __device__ __forceinline__ void load(const F8QuantizeArgs& a, int64_t at, int64_t scale_at, int64_t) {
-    // (codes past the columns are no values: their column is not written)
-    w = load_wide<A>(reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.x) + at));
-    byte = a.x_scales[scale_at];
-  }
-  __device__ __forceinline__ void zero() {
-    w = u32x2{0, 0};
-    byte = 0;
-  }
   __device__ __forceinline__ void four(int h, float (&v)[4]) const {
     const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], block_factor(byte), false);
     const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], block_factor(byte), true);
     v[0] = lo[0]; v[1] = lo[1]; v[2] = hi[0]; v[3] = hi[1];
   }
-  __device__ __forceinline__ bool none() const { return byte == 255u; }  // the block is NaN
 };
+
+// Lane P of each 16 in all of them.
+template <int P>
+__device__ __forceinline__ uint32_t row16_lane(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x150 + P, 0xf, 0xf, true));
+}
 
 // The squares' order: workgroup b runs on XCD b mod 8 and takes place b / 8 of
 // that XCD's contiguous share; the order goes down kBands bands of rows, then
@@ -133,21 +122,43 @@ __device__ __forceinline__ bool square_of(const Squares& q, uint32_t block, uint
   return true;
 }
 
-template <int SRC, int A>
-__global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, Squares squares) {
-  __shared__ __attribute__((aligned(16))) uint32_t most[4][128];
-  __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 128];
-  uint32_t band, kb;
-  if (!square_of(squares, blockIdx.y * kGridX + blockIdx.x, band, kb)) return;
-  const int64_t row0 = static_cast<int64_t>(band) * 128, col0 = static_cast<int64_t>(kb) * 128;
+// One square.  rows, cols: what of it is inside the matrix; WHOLE: all of it
+// (no comparison per row then; address arithmetic and comparisons, not memory,
+// bounded the kernel: pointers are made once per thread and go on by scalars).
+template <int SRC, int A, bool WHOLE>
+__device__ __forceinline__ void square_body(const F8QuantizeArgs& a, uint32_t band, uint32_t kb, int rows, int cols,
+                                            uint32_t (&most)[4][128], uint8_t (&turned)[128 * 128]) {
   const int t = threadIdx.x, c8 = t & 15, rg = t >> 4, wave = t >> 6;
-  const int64_t spitch = f8_scale_pitch(a.cols), col = col0 + 8 * c8, row_at = row0 + 8 * rg;
+  const int64_t row0 = static_cast<int64_t>(band) * 128, col0 = static_cast<int64_t>(kb) * 128;
+  const int64_t spitch = f8_scale_pitch(a.cols);
+  const int left = WHOLE ? 8 : cols - 8 * c8;  // columns from the thread's first on
+  auto inside = [&](int p) { return WHOLE || (8 * rg + p < rows && left > 0); };
   Piece<SRC> in[8];
+  if constexpr (SRC == PT_F8) {
+    const uint8_t* const x = static_cast<const uint8_t*>(a.x) + (row0 + 8 * rg) * a.ldx + col0 + 8 * c8;
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    in[p].zero();
-    if (row_at + p < a.rows && col < a.cols)
-      in[p].template load<A>(a, row_at * a.ldx + col + p * a.ldx, (row_at + p) * spitch + kb, col);
+    for (int p = 0; p < 8; ++p)
+      // (codes past the columns are no values: their column is not written)
+      in[p].w = inside(p) ? load_wide<A>(reinterpret_cast<const u32x2*>(x + p * a.ldx)) : u32x2{0, 0};
+    // the scales of the thread's rows: one per lane, handed on
+    uint32_t bytes = 0;
+    if (c8 < 8 && (WHOLE || 8 * rg + c8 < rows)) bytes = a.x_scales[(row0 + 8 * rg + c8) * spitch + kb];
+    in[0].byte = row16_lane<0>(bytes);
+    in[1].byte = row16_lane<1>(bytes);
+    in[2].byte = row16_lane<2>(bytes);
+    in[3].byte = row16_lane<3>(bytes);
+    in[4].byte = row16_lane<4>(bytes);
+    in[5].byte = row16_lane<5>(bytes);
+    in[6].byte = row16_lane<6>(bytes);
+    in[7].byte = row16_lane<7>(bytes);
+  } else {
+    constexpr int es = SRC == PT_F32 ? 4 : 2;
+    const uint8_t* const x = static_cast<const uint8_t*>(a.x) + ((row0 + 8 * rg) * a.ldx + col0 + 8 * c8) * es;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      in[p].raw.zero();
+      if (inside(p)) in[p].raw.template load<A>(x + p * a.ldx * es, 0, left);
+    }
   }
   // magnitudes: of the thread's rows (rm) and columns (cm)
   uint32_t rm[8], cm[8];
@@ -172,21 +183,24 @@ __global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, S
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) cm[j] = 0;
+    bool none = false;  // a row's block is NaN
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       rm[p] = 0;
+      if constexpr (SRC == PT_F8) none |= in[p].byte == 255u;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[4];
         in[p].four(h, v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t m = in[p].none() ? 0x7f800000u : magnitude(v[j]);
-          rm[p] = max(rm[p], m);
-          cm[4 * h + j] = max(cm[4 * h + j], m);
+          rm[p] = max(rm[p], magnitude(v[j]));
+          cm[4 * h + j] = max(cm[4 * h + j], magnitude(v[j]));
         }
       }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cm[j] = none ? 0x7f800000u : cm[j];
   }
   // columns: over the wave's four groups of rows, then over the waves
 #pragma unroll
@@ -211,12 +225,14 @@ __global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, S
   }
   if constexpr (SRC != PT_F8) {
     if (a.codes) {
-      const int64_t pitch = f8_pitch(a.cols), blocks = pitch / kF8Block;
+      const int64_t pitch = f8_pitch(a.cols);
+      uint8_t* const to = a.codes + (row0 + 8 * rg) * pitch + col0 + 8 * c8;
+      uint32_t own = 0;  // the scale byte of row 8 rg + c8
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
-        const int64_t row = row_at + p;
         const uint32_t byte = block_byte(a.square ? all : row16_max(rm[p]));
-        if (row >= a.rows) continue;
+        own = c8 == p ? byte : own;
+        if (!WHOLE && 8 * rg + p >= rows) continue;  // (past the columns: zeros up to the pitch)
         u32x2 w;
         if constexpr (SRC == PT_BF16) {
           w = pack8_bf16(in[p].raw.w, block_factor(byte));
@@ -226,14 +242,19 @@ __global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, S
           w = pack8(v, block_factor(byte));
         }
         if (byte == 255u) w = u32x2{0, 0};
-        store_wide<A>(reinterpret_cast<u32x2*>(a.codes + row_at * pitch + col + p * pitch), w);
-        if (c8 == 0) a.scales[row * spitch + kb] = static_cast<uint8_t>(byte);
-        if (kb == blocks - 1 && c8 < spitch - blocks) a.scales[row * spitch + blocks + c8] = 0;
+        store_wide<A>(reinterpret_cast<u32x2*>(to + p * pitch), w);
       }
+      uint8_t* const s = a.scales + (row0 + 8 * rg) * spitch;
+      if (c8 < 8 && (WHOLE || 8 * rg + c8 < rows)) s[c8 * spitch + kb] = static_cast<uint8_t>(own);
+      const int64_t blocks = pitch / kF8Block;
+      if (kb == blocks - 1 && c8 < spitch - blocks)
+        for (int p = 0; p < 8; ++p)
+          if (8 * rg + p < rows) s[p * spitch + blocks + c8] = 0;
     }
   }
   if (!a.codes_t) return;
   const int64_t pitch_t = f8_pitch(a.rows), spitch_t = f8_scale_pitch(a.rows), blocks_t = pitch_t / kF8Block;
+  uint32_t own = 0;  // the scale byte of column 8 c8 + rg
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float v[8][4];
@@ -243,25 +264,42 @@ __global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, S
     for (int i = 0; i < 4; ++i) {
       const int j = 4 * h + i;
       const uint32_t byte = block_byte(a.square ? all : cm[j]);
+      own = rg == j ? byte : own;
       const float r[8] = {v[0][i], v[1][i], v[2][i], v[3][i], v[4][i], v[5][i], v[6][i], v[7][i]};
       u32x2 w = pack8(r, block_factor(byte));
       if (byte == 255u) w = u32x2{0, 0};
       // column 8 c8 + j, its rows' pieces of 8 permuted by c8: the 16 columns of a write are on banks of their own
       *reinterpret_cast<u32x2*>(turned + (8 * c8 + j) * 128 + 8 * (rg ^ c8)) = w;
-      if (rg == 0 && col + j < a.cols) a.scales_t[(col + j) * spitch_t + band] = static_cast<uint8_t>(byte);
-      if (band == blocks_t - 1 && rg < spitch_t - blocks_t && col + j < a.cols)
-        a.scales_t[(col + j) * spitch_t + blocks_t + rg] = 0;
     }
   }
+  uint8_t* const s = a.scales_t + (col0 + 8 * c8) * spitch_t;
+  if (rg < 8 && (WHOLE || rg < left)) s[rg * spitch_t + band] = static_cast<uint8_t>(own);
+  if (band == blocks_t - 1 && rg < spitch_t - blocks_t)
+    for (int j = 0; j < 8; ++j)
+      if (j < left) s[j * spitch_t + blocks_t + rg] = 0;
   __syncthreads();
+  uint8_t* const to = a.codes_t + (col0 + (t >> 3)) * pitch_t + row0 + 16 * (t & 7);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int c = (t >> 3) + 32 * i, m = t & 7, perm = c >> 3;
-    if (col0 + c >= a.cols) continue;
+    if (!WHOLE && c >= cols) continue;
     const u32x4 w = *reinterpret_cast<const u32x4*>(turned + c * 128 + 16 * (m ^ (perm >> 1)));
-    store_wide<A>(reinterpret_cast<u32x4*>(a.codes_t + (col0 + c) * pitch_t + row0 + 16 * m),
-                  perm & 1 ? u32x4{w[2], w[3], w[0], w[1]} : w);
+    store_wide<A>(reinterpret_cast<u32x4*>(to + 32 * i * pitch_t), perm & 1 ? u32x4{w[2], w[3], w[0], w[1]} : w);
   }
+}
+
+template <int SRC, int A>
+__global__ __launch_bounds__(kThreads) void f8_square_kernel(F8QuantizeArgs a, Squares squares) {
+  __shared__ __attribute__((aligned(16))) uint32_t most[4][128];
+  __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 128];
+  uint32_t band, kb;
+  if (!square_of(squares, blockIdx.y * kGridX + blockIdx.x, band, kb)) return;
+  const int rows = static_cast<int>(min(a.rows - static_cast<int64_t>(band) * 128, int64_t{128}));
+  const int cols = static_cast<int>(min(a.cols - static_cast<int64_t>(kb) * 128, int64_t{128}));
+  if (rows == 128 && cols == 128)
+    square_body<SRC, A, true>(a, band, kb, rows, cols, most, turned);
+  else
+    square_body<SRC, A, false>(a, band, kb, rows, cols, most, turned);
 }
 
 template <int T, int A>

@@ -202,7 +202,7 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(LayerNormArgs a, int W
 // Waves of a row: the fewest that keep a lane's pieces at four, or, with too
 // few rows to fill the chip, as many as have a piece each.
 static int row_waves(int64_t rows, int d) {
-  const int per_lane = rows >= 2048 ? 4 : 1;
+  const int per_lane = rows >= 2048 ? 2 : 1;
   int W = 1;
   while (W < kMaxWaves && 64 * W * per_lane < d) W *= 2;
   return W;
