@@ -18,7 +18,7 @@ import ctypes
 import torch
 
 from ._binding import DistGemmError, lib
-from ._mx import _BYTES, _SCALES, _device, _flat, _matrix, _rows, _stream_of, _wrong
+from ._mx import _BYTES, _ELEM_OF, _SCALES, _current, _device, _flat, _matrix, _rows, _stream_of, _wrong
 
 LAYER_NORM_OUTPUTS = {"SAME": 0, "E4M3": 1, "F8": 2}
 
@@ -66,19 +66,37 @@ def dist_gemm_f8_scale_pitch(cols: int) -> int:
     return lib.dist_gemm_f8_scale_pitch(cols)
 
 
-def _f8_pair(codes, scales, rows, cols, device, name="", end=""):
-    """Checks the F8 tensor (codes, scales) of rows x cols; its two addresses."""
-    blocks = (cols + 127) // 128
-    _flat(codes, f"{name}codes{end}", _BYTES, rows * blocks * 128, device)
-    _flat(scales, f"{name}scales{end}", _SCALES, rows * ((blocks + 15) // 16 * 16), device)
+# As in _mx.py: each check is one comparison where the argument is right, and
+# the functions that take the argument apart make the message where it is not.
+
+def _first(t, name):
+    """(device, element type, rows, cols, leading dimension) of an operator's first matrix."""
+    d, e = t.get_device(), _ELEM_OF.get(t.dtype)
+    if d < 0 or d != _current() or e is None or t.dim() != 2:
+        _matrix(t, name)
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if s0 < cols or s1 != 1:
+        s0 = _rows(t, name, t.dtype, t.shape, d)
+    return d, e, rows, cols, s0
+
+
+def _f8_pair(codes, scales, rows, blocks, device, name="codes", scales_name="scales"):
+    """Checks an F8 tensor of `rows` rows of `blocks` blocks of 128; its two addresses."""
+    if (codes.dtype not in _BYTES or codes.numel() != rows * blocks * 128 or not codes.is_contiguous()
+            or codes.get_device() != device):
+        _wrong(codes, name, _BYTES, rows * blocks * 128, device)
+    if (scales.dtype not in _SCALES or scales.numel() != rows * ((blocks + 15) // 16 * 16) or not scales.is_contiguous()
+            or scales.get_device() != device):
+        _wrong(scales, scales_name, _SCALES, rows * ((blocks + 15) // 16 * 16), device)
     return codes.data_ptr(), scales.data_ptr()
 
 
-def _pair_or_none(codes, scales, rows, cols, device, name="", end=""):
+def _pair_or_none(codes, scales, rows, blocks, device, name, scales_name):
     if codes is not None and scales is not None:
-        return _f8_pair(codes, scales, rows, cols, device, name, end)
+        return _f8_pair(codes, scales, rows, blocks, device, name, scales_name)
     if codes is not None or scales is not None:
-        raise ValueError(f"{name}codes{end} and {name}scales{end} go together")
+        raise ValueError(f"{name} and {scales_name} go together")
     return None, None
 
 
@@ -96,11 +114,9 @@ def dist_gemm_f8_quantize(x, codes=None, scales=None, codes_t=None, scales_t=Non
     (codes, scales) and / or that of its transpose (codes_t, scales_t).
 
     block_rows = 128: blocks of 128 x 128 share a scale (weights)."""
-    d, e, shape = _matrix(x, "x")
-    rows, cols = shape
-    ld = _rows(x, "x", x.dtype, shape, d)
-    pc, ps = _pair_or_none(codes, scales, rows, cols, d)
-    pct, pst = _pair_or_none(codes_t, scales_t, cols, rows, d, end="_t")
+    d, e, rows, cols, ld = _first(x, "x")
+    pc, ps = _pair_or_none(codes, scales, rows, (cols + 127) // 128, d, "codes", "scales")
+    pct, pst = _pair_or_none(codes_t, scales_t, cols, (rows + 127) // 128, d, "codes_t", "scales_t")
     rc = lib.dist_gemm_f8_quantize(x.data_ptr(), ld, e, rows, cols, block_rows, pc, ps, pct, pst, _stream_of(stream, d))
     if rc:
         _raise(rc)
@@ -108,10 +124,8 @@ def dist_gemm_f8_quantize(x, codes=None, scales=None, codes_t=None, scales_t=Non
 
 def dist_gemm_f8_dequantize(codes, scales, y, stream=None):
     """The values of the F8 tensor (codes, scales) into y (rows x cols, f32 or bf16, rows at any pitch)."""
-    d, e, shape = _matrix(y, "y")
-    rows, cols = shape
-    ld = _rows(y, "y", y.dtype, shape, d)
-    pc, ps = _f8_pair(codes, scales, rows, cols, d)
+    d, e, rows, cols, ld = _first(y, "y")
+    pc, ps = _f8_pair(codes, scales, rows, (cols + 127) // 128, d)
     rc = lib.dist_gemm_f8_dequantize(pc, ps, rows, cols, y.data_ptr(), ld, e, _stream_of(stream, d))
     if rc:
         _raise(rc)
@@ -129,8 +143,8 @@ def dist_gemm_f8_transpose(codes, scales, codes_t, scales_t, stream=None):
     The sizes are the two tensors' rows: codes is rows x pitch(cols), codes_t cols x pitch(rows)."""
     d = _device(codes, "codes")
     rows, cols = _codes(codes, "codes")[0], _codes(codes_t, "codes_t")[0]
-    pc, ps = _f8_pair(codes, scales, rows, cols, d)
-    pct, pst = _f8_pair(codes_t, scales_t, cols, rows, d, end="_t")
+    pc, ps = _f8_pair(codes, scales, rows, (cols + 127) // 128, d)
+    pct, pst = _f8_pair(codes_t, scales_t, cols, (rows + 127) // 128, d, "codes_t", "scales_t")
     rc = lib.dist_gemm_f8_transpose(pc, ps, rows, cols, pct, pst, _stream_of(stream, d))
     if rc:
         _raise(rc)
@@ -146,17 +160,15 @@ def dist_gemm_f8_product(A, A_scales, B, B_scales, D, bias=None, C=None, alpha=1
 
     K is the operands' pitch (their codes' second size); workspace: any GPU
     tensor of at least dist_gemm_f8_product_workspace(M, N, K) bytes."""
-    d, e, shape = _matrix(D, "D")
-    M, N = shape
+    d, e, M, N, ldd = _first(D, "D")
     K = _codes(A, "A")[1]
     if K % 128 or _codes(B, "B")[1] != K:
         raise ValueError(f"A and B must have rows of one pitch (a multiple of 128), have {K} and {B.shape[1]}")
-    ldd = _rows(D, "D", D.dtype, shape, d)
-    pa, pas = _f8_pair(A, A_scales, M, K, d, "A's ")
-    pb, pbs = _f8_pair(B, B_scales, N, K, d, "B's ")
+    pa, pas = _f8_pair(A, A_scales, M, K // 128, d, "A", "A_scales")
+    pb, pbs = _f8_pair(B, B_scales, N, K // 128, d, "B", "B_scales")
     ldc, pc, pbias = 0, None, None
     if C is not None:
-        ldc, pc = _rows(C, "C", D.dtype, shape, d), C.data_ptr()
+        ldc, pc = _rows(C, "C", D.dtype, D.shape, d), C.data_ptr()
     if bias is not None:
         _flat(bias, "bias", (D.dtype,), N, d)
         pbias = bias.data_ptr()
@@ -175,11 +187,9 @@ def dist_gemm_layer_norm(x, weight, bias, y, eps=1e-5, output="SAME", residual=N
     `scale`) or "F8" (y the codes and `scales` the scales of an F8 tensor).
     kept, kept_scales: room for the normalised rows as an F8 tensor, the 8-bit
     checkpoint for the gradient."""
-    d, e, shape = _matrix(x, "x")
+    d, e, rows, cols, ldx = _first(x, "x")
     out = LAYER_NORM_OUTPUTS.get(output, -1)
-    t = x.dtype
-    rows, cols = shape
-    ldx = _rows(x, "x", t, shape, d)
+    t, blocks = x.dtype, (cols + 127) // 128
     _flat(weight, "weight", (t,), cols, d)
     ldr = ldh = ldy = 0
     pr = ph = ps = pm = pt = pbias = None
@@ -187,6 +197,7 @@ def dist_gemm_layer_norm(x, weight, bias, y, eps=1e-5, output="SAME", residual=N
         _flat(bias, "bias", (t,), cols, d)
         pbias = bias.data_ptr()
     if residual is not None and h is not None:
+        shape = x.shape
         ldr, ldh = _rows(residual, "residual", t, shape, d), _rows(h, "h", t, shape, d)
         pr, ph = residual.data_ptr(), h.data_ptr()
     elif residual is not None or h is not None:
@@ -198,18 +209,18 @@ def dist_gemm_layer_norm(x, weight, bias, y, eps=1e-5, output="SAME", residual=N
         _flat(rstd, "rstd", (torch.float32,), rows, d)
         pt = rstd.data_ptr()
     if out == 0:
-        ldy = _rows(y, "y", t, shape, d)
+        ldy = _rows(y, "y", t, x.shape, d)
     elif out == 1:
         if y.dtype not in _BYTES:
-            _wrong(y, "y", _BYTES, tuple(shape), d)
-        ldy = _rows(y, "y", y.dtype, shape, d)
+            _wrong(y, "y", _BYTES, tuple(x.shape), d)
+        ldy = _rows(y, "y", y.dtype, x.shape, d)
     elif out == 2:
         if scales is None:
             raise ValueError("an F8 output needs scales")
-        _, ps = _f8_pair(y, scales, rows, cols, d, "y's ")
+        _, ps = _f8_pair(y, scales, rows, blocks, d, "y")
     else:
         raise ValueError(f"unknown output {output!r}")
-    pk, pks = _pair_or_none(kept, kept_scales, rows, cols, d, "kept ")
+    pk, pks = _pair_or_none(kept, kept_scales, rows, blocks, d, "kept", "kept_scales")
     rc = lib.dist_gemm_layer_norm(x.data_ptr(), ldx, pr, ldr, weight.data_ptr(), pbias, e, rows, cols, eps, out, scale,
                                   y.data_ptr(), ldy, ps, ph, ldh, pm, pt, pk, pks, _stream_of(stream, d))
     if rc:
@@ -229,14 +240,13 @@ def dist_gemm_layer_norm_backward(dy, h, mean, rstd, weight, dx, dweight, dbias,
     h is the normalised stream itself (dy's type, with mean), or with h_scales
     the F8 tensor of the normalised rows that the forward pass kept (mean is
     not used and may be None)."""
-    d, e, shape = _matrix(dy, "dy")
-    t = dy.dtype
-    rows, cols = shape
-    lddy, lddx = _rows(dy, "dy", t, shape, d), _rows(dx, "dx", t, shape, d)
+    d, e, rows, cols, lddy = _first(dy, "dy")
+    t, shape = dy.dtype, dy.shape
+    lddx = _rows(dx, "dx", t, shape, d)
     lddh = 0 if dh is None else _rows(dh, "dh", t, shape, d)
     ldh, phs, pm, pdb = 0, None, None, None
     if h_scales is not None:
-        ph, phs = _f8_pair(h, h_scales, rows, cols, d, "h's ")
+        ph, phs = _f8_pair(h, h_scales, rows, (cols + 127) // 128, d, "h", "h_scales")
     else:
         ldh, ph = _rows(h, "h", t, shape, d), h.data_ptr()
         if mean is None:

@@ -6,6 +6,7 @@
 // code * 2^(b - 127) (b = 255: the block is NaN), a row of scales taking
 // f8_scale_pitch(cols) bytes.
 #pragma once
+#include "f8_shape.h"
 #include "mx_common.h"
 #include "mx_shape.h"
 
@@ -79,10 +80,12 @@ hipError_t launch_layer_norm(int type, int out, const LayerNormArgs& a, hipStrea
 int64_t layer_norm_backward_blocks(int64_t rows, int64_t cols);
 hipError_t launch_layer_norm_backward(int type, const LayerNormBackwardArgs& a, hipStream_t st);
 // Products: MxGemmArgs with F8 operands (no groups); work: of f8_gemm_workspace bytes.
-int64_t f8_gemm_workspace(int64_t M, int64_t N, int64_t K, int cus);
 hipError_t launch_f8_gemm(const MxGemmArgs& a, float* work, hipStream_t st);
-// on tiles of `size` (256 or 128) squared
+// on tiles of 256 x 256, 128 x 128 or (size 64) 64 x 128
 hipError_t launch_f8_gemm_tile(int size, const MxGemmArgs& a, hipStream_t st);
+// on tiles of 64 x 128 with K in `parts` (f8_parts of it: every part has some of K), whose sums go through `sums`, parts
+// x M rows of `pitch` values (a multiple of 4)
+hipError_t launch_f8_gemm_split(const MxGemmArgs& a, int parts, float* sums, int64_t pitch, hipStream_t st);
 
 #if defined(__HIPCC__)
 namespace f8 {

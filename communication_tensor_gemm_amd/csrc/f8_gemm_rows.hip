@@ -249,17 +249,14 @@ static hipError_t rows_t(const MxGemmArgs& a, hipStream_t st) {
 
 }  // namespace f8
 
-int64_t f8_gemm_workspace(int64_t, int64_t, int64_t, int) { return 0; }
-
-hipError_t launch_f8_gemm(const MxGemmArgs& a, float*, hipStream_t st) {
+hipError_t launch_f8_gemm(const MxGemmArgs& a, float* work, hipStream_t st) {
   if (a.M == 0) return hipSuccess;
-  if (a.M <= 16) return f8::rows_t<1>(a, st);
-  if (a.M <= 32) return f8::rows_t<2>(a, st);
-  if (a.M <= 64) return f8::rows_t<4>(a, st);
-  auto tiles = [&](int64_t size) { return (a.M + size - 1) / size * ((a.N + size - 1) / size); };
-  auto rounds = [&](int64_t size) { return (tiles(size) + a.cus - 1) / a.cus; };
-  if (tiles(128) <= a.cus / 8 || (tiles(128) <= a.cus / 4 && a.K > 4096)) return f8::rows_lds_t<2, 2, false>(a, st);
-  return launch_f8_gemm_tile(3 * rounds(256) <= rounds(128) ? 256 : 128, a, st);
+  const F8Choice c = f8_choice(a.M, a.N, a.K, a.cus);
+  if (c.rows == 16) return f8::rows_t<1>(a, st);
+  if (c.rows == 32) return a.M <= 32 ? f8::rows_t<2>(a, st) : f8::rows_lds_t<2, 2, false>(a, st);
+  if (c.rows == 64) return f8::rows_t<4>(a, st);
+  if (c.parts > 1) return launch_f8_gemm_split(a, c.parts, work, f8_split_pitch(a.N), st);
+  return launch_f8_gemm_tile(c.size, a, st);
 }
 
 }  // namespace dg

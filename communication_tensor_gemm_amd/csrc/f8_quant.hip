@@ -108,7 +108,7 @@ __device__ __forceinline__ uint32_t row16_lane(uint32_t v) {
 // that XCD's contiguous share; the order goes down kBands bands of rows, then
 // one square to the right, so that the bytes of a line of scales (one per square,
 // of either tensor) meet in one L2.
-constexpr uint32_t kXcds = 8, kBands = 16;
+constexpr uint32_t kXcds = 8, kBands = 8;
 struct Squares {
   uint32_t bands, across;
 };

@@ -136,24 +136,17 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(LayerNormArgs a, int W
   if (W > 1) {
     if ((threadIdx.x & 63) == 0) parts[wave] = f32x2{mean, m2};
     __syncthreads();
-    const int first = wave - part;
-    float total = 0.0f;
-    for (int i = 0; i < W; ++i) {
-      int n = 0;
+    // a part to a lane (a loop over the parts would wait for LDS once per part)
+    const int i = threadIdx.x & 63;
+    int n = 0;
 #pragma unroll
-      for (int c = 0; c < V; ++c) n += min(max(a.cols - 8 * (c * span + i * 64), 0), 512);
-      total = __builtin_fmaf(static_cast<float>(n), parts[first + i][0], total);
-    }
-    mean = total / static_cast<float>(a.cols);
-    m2 = 0.0f;
-    for (int i = 0; i < W; ++i) {
-      int n = 0;
-#pragma unroll
-      for (int c = 0; c < V; ++c) n += min(max(a.cols - 8 * (c * span + i * 64), 0), 512);
-      const f32x2 p = parts[first + i];
-      const float e = p[0] - mean;
-      m2 += n > 0 ? __builtin_fmaf(static_cast<float>(n) * e, e, p[1]) : 0.0f;
-    }
+    for (int c = 0; c < V; ++c) n += min(max(a.cols - 8 * (c * span + i * 64), 0), 512);
+    n = i < W ? n : 0;
+    const f32x2 p = n > 0 ? parts[wave - part + i] : f32x2{0.0f, 0.0f};
+    const float count_i = static_cast<float>(n);
+    mean = wave_total(count_i * p[0]) / static_cast<float>(a.cols);
+    const float e = p[0] - mean;
+    m2 = wave_total(n > 0 ? __builtin_fmaf(count_i * e, e, p[1]) : 0.0f);
   }
   if (!live) return;
   const float rstd = 1.0f / sqrtf(m2 / static_cast<float>(a.cols) + a.eps);
@@ -408,12 +401,11 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBack
       // two sets of slots: a wave may be one turn ahead of another's reads
       if ((threadIdx.x & 63) == 0) red[k & 1][wave] = f32x2{sg, sgn};
       __syncthreads();
-      sg = sgn = 0.0f;
-      for (int i = 0; i < W; ++i) {
-        const f32x2 p = red[k & 1][wave - part + i];
-        sg += p[0];
-        sgn += p[1];
-      }
+      // a wave's sums to a lane (a loop over them would wait for LDS once per wave)
+      const int i = threadIdx.x & 63;
+      const f32x2 p = i < W ? red[k & 1][wave - part + i] : f32x2{0.0f, 0.0f};
+      sg = wave_total(p[0]);
+      sgn = wave_total(p[1]);
     }
     sg *= inv_n;
     sgn *= inv_n;

@@ -111,14 +111,15 @@ struct Geo {
   static constexpr bool kMixed = A8 && !B8;
   static constexpr int kRowB = kMixed ? 64 : 128;  // bytes of a row of B per slab
   static constexpr int SA = TM * 128, SB = TN * kRowB, kStage = SA + SB;
-  static constexpr int kStages = kMixed ? 3 : 2;
-  static constexpr int kScales = (TM + TN) * 16;
+  static constexpr int kStages = kMixed ? 3 : NBM == 1 ? 4 : 2;
+  // scales: 64 rows to a load, the same number of loads for each wave (64 x 128: wave 3's has no rows)
+  static constexpr int LS = ((TM + TN) * 16 + 4095) / 4096, kScales = LS * 4096;
   static constexpr int kLds = kStages * kStage + 2 * kScales;
-  static constexpr int LA = SA / 4096, LB = SB / 4096, LS = kScales / 4096;  // loads per wave
+  static constexpr int LA = SA / 4096, LB = SB / 4096;  // loads per wave
   static constexpr int kScaleK = B8 ? 128 : 32, kChunkK = 16 * kScaleK;      // elements of a scale, of a chunk of scales
   static constexpr int kPerChunk = kChunkK / kSlabK;                         // slabs per chunk of scales
   static constexpr int kSteps = A8 ? 1 : 2;                                  // MFMAs of a block per half slab
-  static constexpr int kWgs = NBM * NBN == 16 ? 1 : 2;                       // workgroups per CU
+  static constexpr int kWgs = NBM == 2 ? 2 : 1;                              // workgroups per CU
   static constexpr int kStores = NBM * NBN * 2;                              // of a whole bf16 wave block
 };
 
@@ -275,8 +276,9 @@ __device__ __forceinline__ bool store_block_of(const MxGemmArgs& p, const Place&
 }
 
 // A workgroup's share of the launch.  KG = 2: of its one tile, two groups of four
-// waves compute half of K each.
-template <bool A8, bool B8, bool kBf16, int NBM, int NBN, int KG>
+// waves compute half of K each.  kSplit: the workgroups of blockIdx.y compute
+// that part of K, whose sums are rows blockIdx.y * M .. of D.
+template <bool A8, bool B8, bool kBf16, int NBM, int NBN, int KG, bool kSplit = false>
 __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* const all_smem) {
   using G = Geo<A8, B8, NBM, NBN>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
@@ -291,11 +293,14 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* const al
   const uint32_t lda = static_cast<uint32_t>(A8 ? p.K : p.K / 2), ldb = static_cast<uint32_t>(B8 ? p.K : p.K / 2);
   // bytes of a row of scales: their number rounded up to 16
   const uint32_t pitch = static_cast<uint32_t>(B8 ? (p.K / G::kScaleK + 15) / 16 * 16 : scale_pitch(p.K));
-  // KG = 2: the first group takes whole 512 elements (of scales, whole dwords), the
-  // second what is left, K elements from kfrom on, and slabs of zeros up to the
-  // first one's number
-  const int each = (p.K + 512 * KG - 1) / (512 * KG) * 512, kfrom = kg * each;
-  const int K = KG == 1 ? static_cast<int>(p.K) : min(static_cast<int>(p.K) - kfrom, each);
+  // parts of K: each takes whole 512 elements (of scales, whole dwords), the last
+  // what is left, K elements from kfrom on.  KG = 2: and slabs of zeros up to the
+  // first group's number
+  static_assert(!kSplit || (B8 && KG == 1), "K is split one way");
+  constexpr bool kAllK = KG == 1 && !kSplit;
+  const int parts = kSplit ? static_cast<int>(gridDim.y) : KG, part = kSplit ? static_cast<int>(blockIdx.y) : kg;
+  const int each = (p.K + 512 * parts - 1) / (512 * parts) * 512, kfrom = kAllK ? 0 : part * each;
+  const int K = kAllK ? static_cast<int>(p.K) : min(static_cast<int>(p.K) - kfrom, each);
   const int KT = ((KG == 1 ? K : each) + G::kSlabK - 1) / G::kSlabK, KC = ((KG == 1 ? K : each) + G::kChunkK - 1) / G::kChunkK;
   const bool partial = (!B8 || KG > 1) && KT * G::kSlabK != K;  // (K of F8 operands is whole slabs)
   const uint32_t afrom = A8 ? kfrom : kfrom / 2, bfrom = B8 ? kfrom : kfrom / 2, sfrom = kfrom / G::kScaleK;  // bytes of a row
@@ -306,16 +311,17 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* const al
   __amdgpu_buffer_rsrc_t rA, rB, rS;
   auto slabs_of = [&](const Place& q) {
     const MxGemmArgs p = fresh_args();
-    // no tile: no bytes, also with the second half's offset
-    rA = make_rsrc(p.A + static_cast<int64_t>(q.row0) * lda + afrom, KG == 1 || q.rows ? q.rows * lda - afrom : 0);
-    rB = make_rsrc(p.B + (q.b_row0 + q.n0) * ldb + bfrom, KG == 1 || q.rows ? q.cols * ldb - bfrom : 0);
+    // no tile: no bytes, also with a part's offset
+    rA = make_rsrc(p.A + static_cast<int64_t>(q.row0) * lda + afrom, kAllK || q.rows ? q.rows * lda - afrom : 0);
+    rB = make_rsrc(p.B + (q.b_row0 + q.n0) * ldb + bfrom, kAllK || q.rows ? q.cols * ldb - bfrom : 0);
   };
-  // waves 0, 1 load scales of A, 2, 3 of B
-  const bool scale_a = wave < 2;
+  // the first waves load scales of A, the others of B
+  const int scale_row = wave * 64 * G::LS;
+  const bool scale_a = scale_row < G::TM;
   auto scales_of = [&](const Place& q) {
     const MxGemmArgs p = fresh_args();
     rS = make_rsrc((scale_a ? p.As + static_cast<int64_t>(q.row0) * pitch : p.Bs + (q.b_row0 + q.n0) * pitch) + sfrom,
-                   KG == 1 || q.rows ? (scale_a ? q.rows : q.cols) * pitch - sfrom : 0);
+                   kAllK || q.rows ? (scale_a ? q.rows : q.cols) * pitch - sfrom : 0);
   };
   // lane offsets: 128-byte rows in even and odd blocks of 8 rows, 64-byte rows in blocks of 16
   const int piece = lane & 3, r16 = lane >> 2;
@@ -327,7 +333,7 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* const al
     gb[odd] = G::kMixed ? (16 * G::LB * wave + r16) * ldb + 16 * (piece ^ row_perm(r16))
                  : (8 * G::LB * wave + 8 * odd + (r16 & 7)) * ldb + byte_in_slab(odd);
   }
-  const uint32_t gs = static_cast<uint32_t>((scale_a ? wave : wave - 2) * 64 * G::LS + lane) * pitch;
+  const uint32_t gs = static_cast<uint32_t>(scale_row - (scale_a ? 0 : G::TM) + lane) * pitch;
   int lkt = 0;
   // before the loads of slab lkt, K not a multiple of the slab: the last
   // slabs' pieces past K out of range, the first slab's back in
@@ -574,8 +580,10 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* const al
     // what the barrier waits for: the next slab has landed, and so has the next
     // chunk of scales if it is read now.  Operations retire in order, and behind
     // the next slab's loads are those of the slabs after it, a tile's stores
-    // and the scales' loads.
-    const int wait = last && kt % G::kPerChunk == 0 ? 2 : kt == 0 && behind ? 1 : 0;
+    // and the scales' loads.  (A chunk loaded no more than kSoon slabs ago need
+    // not have landed yet.)
+    constexpr int kSoon = G::kStages > 3 ? G::kStages - 3 : 0;
+    const int wait = last && kt % G::kPerChunk <= kSoon ? 2 : kt == 0 && behind ? 1 : 0;
     wait_lgkmcnt0();
     if constexpr (A8) {
 #pragma unroll
@@ -636,6 +644,7 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* const al
       }
       int elane = lane;  // the epilogue's addresses are not hoisted above the loop
       asm volatile("" : "+v"(elane));
+      if constexpr (kSplit) cur.row0 += static_cast<int32_t>(blockIdx.y) * p.M;
       behind = store_block_of<kBf16, NBM, NBN>(fresh_args(), cur, wm, wn, elane, acc);
       if (KG == 2 || next.rows == 0) return;
       clear();

@@ -25,9 +25,10 @@ def listings(tmp_path_factory):
         return [_kernels(t) for t in ex.map(lambda s: _device_asm(B, s, str(tmp / (s + ".s"))), srcs)]
 
 
-def geometry(bf16, nb):
-    """128 bytes per row of both operands in a slab, two stages; a chunk of 16 scale bytes per row."""
-    return dict(loads=2 * (64 * nb * 128 // 4096), stages=2, scales=2 * 64 * nb * 16 // 4096, stores=2 * nb * nb if bf16 else 0)
+def geometry(bf16, nbm, nbn):
+    """128 bytes per row of both operands in a slab, two stages (four of 64 x 128); a chunk of 16 scale bytes per row."""
+    rows = 64 * (nbm + nbn)
+    return dict(loads=rows * 128 // 4096, stages=4 if nbm == 1 else 2, scales=-(-rows * 16 // 4096), stores=2 * nbm * nbn if bf16 else 0)
 
 
 def test_few_rows(listings):
@@ -45,13 +46,14 @@ def test_few_rows(listings):
 def test_tiles(listings):
     checked = 0
     for name, body in listings[1].items():
-        m = re.search(r"f8_gemm_tile_kernelILb(\d)ELi(\d)ELi(\d)ELi(\d)E", name)
+        m = re.search(r"f8_gemm_tile_kernelILb(\d)ELi(\d)ELi(\d)ELi(\d)ELb(\d)E", name)
         if not m:
             continue
-        assert m.group(2) == m.group(3), name
-        g = geometry(m.group(1) == "1", int(m.group(2)))
+        nbm, nbn = int(m.group(2)), int(m.group(3))
+        assert (nbm, nbn) in ((4, 4), (2, 2), (1, 2)), name
+        g = geometry(m.group(1) == "1", nbm, nbn)
         ev = events(body)
-        if int(m.group(4)) == 1:
+        if int(m.group(4)) == 1:         # (not of two groups of waves)
             # K is whole slabs: no branch stands between the scales' loads and the first stage's
             ev.insert([i for i, e in enumerate(ev) if e == "L"][g["scales"] - 1] + 1, "|")
         assert tile_ok(ev, **g), (name, g)
@@ -59,7 +61,7 @@ def test_tiles(listings):
             for i in [k for k, e in enumerate(ev) if e == what]:
                 assert not tile_ok(ev[:i] + ev[i + 1:], **g), (name, i)
         checked += 1
-    assert checked == 2 * 3                  # outputs, tile sizes and split K
+    assert checked == 2 * 4 + 1              # outputs, by tile sizes and two groups of waves; K in parts into fp32
 
 
 def test_no_kernel_reads_spilled_registers(listings):

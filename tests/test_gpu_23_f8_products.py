@@ -85,7 +85,11 @@ def dense(M, N, K, out, seed=1, alpha=1.0, beta=0.0, with_bias=False, pitch=None
 
 SIZES = [(1, 1, 1), (1, 16, 128), (3, 5, 96), (16, 48, 512), (17, 33, 544), (1, 272, 4096), (31, 100, 992), (33, 64, 1536),
          (2, 100, 16384), (5, 40, 20000), (64, 130, 2080), (65, 257, 160), (100, 300, 1024), (129, 128, 3584), (200, 520, 608),
-         (256, 256, 256), (300, 700, 1120), (513, 260, 512), (700, 1030, 2048), (150, 500, 6000), (520, 530, 4224), (140, 900, 128)]
+         (256, 256, 256), (300, 700, 1120), (513, 260, 512), (700, 1030, 2048), (150, 500, 6000), (520, 530, 4224), (140, 900, 128),
+         # K in parts
+         (70, 130, 20000), (33, 60, 16400), (130, 300, 16500), (513, 700, 12000), (300, 1000, 30000),
+         # more than a tile of 64 x 128 per CU
+         (2100, 1100, 200), (1000, 3000, 384)]
 
 
 @pytest.mark.parametrize("out", ["BF16", "F32"])
@@ -94,7 +98,7 @@ def test_dense(M, N, K, out):
     dense(M, N, K, out)
 
 
-@pytest.mark.parametrize("M,N,K", [(2, 40, 96), (24, 100, 544), (60, 33, 1024), (150, 200, 2080), (600, 1000, 640), (130, 260, 5000)])
+@pytest.mark.parametrize("M,N,K", [(2, 40, 96), (24, 100, 544), (60, 33, 1024), (150, 200, 2080), (600, 1000, 640), (130, 260, 5000), (130, 260, 20000), (2200, 1030, 300)])
 def test_small_products_are_exact(M, N, K):
     """Scales all 1 and codes of whole numbers up to 8: every sum is a whole number under 2^23, so fp32 holds it exactly."""
     import torch
@@ -107,7 +111,7 @@ def test_small_products_are_exact(M, N, K):
     assert np.array_equal(f64(D), a @ b.T)
 
 
-@pytest.mark.parametrize("M,N,K", [(8, 64, 1024), (3, 50, 4096), (40, 70, 5120), (140, 200, 512), (600, 520, 512), (130, 200, 6400)])
+@pytest.mark.parametrize("M,N,K", [(8, 64, 1024), (3, 50, 4096), (40, 70, 5120), (140, 200, 512), (600, 520, 512), (130, 200, 6400), (130, 200, 20480), (400, 520, 16384)])
 def test_every_block_has_its_own_scale(M, N, K):
     """One element of A set per row, another block each: D is that element's
     value times its column of B, so a scale taken from a neighbour shows."""
@@ -123,7 +127,7 @@ def test_every_block_has_its_own_scale(M, N, K):
 
 
 @pytest.mark.parametrize("out", ["BF16", "F32"])
-@pytest.mark.parametrize("M,N,K", [(5, 70, 544), (50, 64, 5120), (130, 300, 512), (520, 512, 512), (140, 260, 6400)])
+@pytest.mark.parametrize("M,N,K", [(5, 70, 544), (50, 64, 5120), (130, 300, 512), (520, 512, 512), (140, 260, 6400), (140, 262, 20000), (130, 301, 17000)])
 def test_alpha_beta_bias(M, N, K, out):
     dense(M, N, K, out, alpha=0.5, beta=-2.0, with_bias=True, pitch=N + 5)
     dense(M, N, K, out, alpha=-1.5, with_bias=True, pitch=N + 8)
@@ -142,7 +146,7 @@ def test_without_beta_c_is_not_read():
 
 
 @pytest.mark.parametrize("M", [4, 50, 200, 600])
-@pytest.mark.parametrize("K", [300, 6400])
+@pytest.mark.parametrize("K", [300, 6400, 24000])
 def test_nan_blocks_reach_their_rows_and_columns_alone(M, K):
     import torch
     A, As, a = make(M, K, 1)
@@ -160,7 +164,7 @@ def test_nan_blocks_reach_their_rows_and_columns_alone(M, K):
 
 
 @pytest.mark.parametrize("M", [3, 40, 200, 520])
-@pytest.mark.parametrize("K", [300, 6400])
+@pytest.mark.parametrize("K", [300, 6400, 24000])
 def test_scale_bytes_past_the_blocks_do_not_count(M, K):
     import torch
     A, As, a = make(M, K, 1)
@@ -197,12 +201,12 @@ def test_no_rows():
 
 
 def test_the_same_from_run_to_run():
-    for M, N, K in ((3, 1000, 4096), (200, 1024, 7168), (520, 1024, 1024)):
+    for M, N, K in ((3, 1000, 4096), (200, 1024, 7168), (520, 1024, 1024), (300, 300, 20480)):
         r = [dense(M, N, K, "F32")[0] for _ in range(3)]
         assert np.array_equal(r[0], r[1]) and np.array_equal(r[0], r[2])
 
 
-@pytest.mark.parametrize("M,N,K", [(7, 300, 1100), (100, 300, 1100), (200, 1024, 7168), (700, 700, 700)])
+@pytest.mark.parametrize("M,N,K", [(7, 300, 1100), (100, 300, 1100), (200, 1024, 7168), (700, 700, 700), (200, 500, 20480)])
 def test_on_a_stream_of_its_own_and_in_a_graph(M, N, K):
     import torch
     A, As, a = make(M, K, 1)
@@ -262,3 +266,26 @@ def test_refusals_of_tensors():
                 dict(A=good["A"].reshape(-1))):
         with pytest.raises((ValueError, dg.DistGemmError)):
             dg.dist_gemm_f8_product(**{**good, **bad})
+
+
+def test_parts_are_what_these_sizes_take():
+    """The sizes above that stand for K in parts have a workspace, and one that is too small, missing or misaligned is refused."""
+    import torch
+    for M, N, K in ((70, 130, 20096), (33, 60, 16512), (130, 300, 16512), (513, 700, 12032), (200, 130, 24064), (40, 130, 24064)):
+        assert dg.dist_gemm_f8_product_workspace(M, N, K) > 0
+    assert dg.dist_gemm_f8_product_workspace(64, 64, 100) == 0 and dg.dist_gemm_f8_product_workspace(-1, 64, 128) == 0
+    M, N, K = 130, 300, 16512
+    A, As, a = make(M, K, 1)
+    B, Bs, b = make(N, K, 2)
+    n = dg.dist_gemm_f8_product_workspace(M, N, K)
+    ws = torch.empty(n + 16, dtype=torch.uint8, device="cuda")
+    D = torch.empty((M, N), device="cuda")
+    args = (up(A), up(As), up(B), up(Bs), D)
+    for bad in (None, ws[:n - 1], ws[8:], ws[:0], ws.cpu(), ws[::2]):
+        with pytest.raises((ValueError, dg.DistGemmError)):
+            dg.dist_gemm_f8_product(*args, workspace=bad)
+    with pytest.raises(dg.DistGemmError, match="alias"):
+        big = torch.empty((n // 1200 + 1) * 300, device="cuda")
+        dg.dist_gemm_f8_product(*args[:4], big[:M * N].view(M, N), workspace=big)
+    dg.dist_gemm_f8_product(*args, workspace=ws[:n])
+    check(f64(D), a, b, "F32")
