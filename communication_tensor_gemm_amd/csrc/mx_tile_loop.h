@@ -218,7 +218,10 @@ __device__ __forceinline__ Place place_of(Tiles t, int32_t at) {
 // stores 32 rows of 32 bytes, those past the last row out of the descriptor's
 // range (kStores instructions in all, and true is returned); else four columns
 // at a time.  No LDS: the next tile's slabs are in it.
-template <bool kBf16, int NBM, int NBN>
+// kWideC: C and bias, where they are aligned to it, are read four columns at a
+// time, and a block of whole columns has its four reads of C under way at once (not
+// with two groups of waves, whose registers it would spill).
+template <bool kBf16, int NBM, int NBN, bool kWideC>
 __device__ __forceinline__ bool store_block_of(const MxGemmArgs& p, const Place& at, int wm, int wn, int lane,
                                                f32x16 (&acc)[NBM][NBN]) {
   constexpr int WM = 32 * NBM, WN = 32 * NBN;
@@ -227,6 +230,10 @@ __device__ __forceinline__ bool store_block_of(const MxGemmArgs& p, const Place&
   const bool whole = kBf16 && at.cols - wcol >= WN && p.beta == 0.0f && p.ldd < (1 << 22) &&
                      ((reinterpret_cast<uint64_t>(p.D) | (static_cast<uint64_t>(p.ldd) * 2)) & 15) == 0;
   const bool wide = wide_rows<kBf16>(p);
+  constexpr uint64_t es = kBf16 ? 2 : 4;
+  const bool wide_in = kWideC && wide && at.cols - wcol >= WN && (p.beta != 0.0f || p.bias) &&
+                       (p.beta == 0.0f || ((reinterpret_cast<uint64_t>(p.C) | static_cast<uint64_t>(p.ldc) * es) & (4 * es - 1)) == 0) &&
+                       (!p.bias || ((reinterpret_cast<uint64_t>(p.bias) + static_cast<uint64_t>(at.b_row0 + at.n0) * es) & (4 * es - 1)) == 0);
   const uint32_t pitch = whole ? static_cast<uint32_t>(p.ldd) * 2 : 0;
   const auto rD = make_rsrc(static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(at.row0) * p.ldd + at.n0) * 2, at.rows * pitch);
 #pragma unroll
@@ -261,6 +268,37 @@ __device__ __forceinline__ bool store_block_of(const MxGemmArgs& p, const Place&
           const auto x = __builtin_amdgcn_permlane32_swap(w[g][0], w[g + 1][0], false, false);
           const auto y = __builtin_amdgcn_permlane32_swap(w[g][1], w[g + 1][1], false, false);
           __builtin_amdgcn_raw_buffer_store_b128(u32x4{x[0], y[0], x[1], y[1]}, rD, d + 16 * g, 0, 0);
+        }
+      } else if (kWideC && wide_in) {
+        if (r < at.rows) {
+          const int64_t row = at.row0 + r;
+          const int32_t c = at.n0 + c0 + 4 * eh;
+          f32x4 v[4], in[4], b[4];
+          if (p.beta != 0.0f) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) in[g] = load_four<kBf16>(p.C, row * p.ldc + c + 8 * g);
+          }
+          if (p.bias) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) b[g] = load_four<kBf16>(p.bias, at.b_row0 + c + 8 * g);
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float o = p.alpha * acc[i][j][4 * g + e];
+              if (p.beta != 0.0f) o = __builtin_fmaf(p.beta, in[g][e], o);
+              if (p.bias) o += b[g][e];
+              v[g][e] = o;
+            }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int64_t to = row * p.ldd + c + 8 * g;
+            if constexpr (kBf16)
+              *(global_ptr<u32x2>)((global_ptr<uint16_t>)p.D + to) = u32x2{pack_bf16(v[g][0], v[g][1]), pack_bf16(v[g][2], v[g][3])};
+            else
+              *(global_ptr<f32x4>)((global_ptr<float>)p.D + to) = v[g];
+          }
         }
       } else if (r < at.rows) {
 #pragma unroll
@@ -645,7 +683,7 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, uint8_t* const al
       int elane = lane;  // the epilogue's addresses are not hoisted above the loop
       asm volatile("" : "+v"(elane));
       if constexpr (kSplit) cur.row0 += static_cast<int32_t>(blockIdx.y) * p.M;
-      behind = store_block_of<kBf16, NBM, NBN>(fresh_args(), cur, wm, wn, elane, acc);
+      behind = store_block_of<kBf16, NBM, NBN, B8 && KG == 1>(fresh_args(), cur, wm, wn, elane, acc);
       if (KG == 2 || next.rows == 0) return;
       clear();
       at += tiles.step;

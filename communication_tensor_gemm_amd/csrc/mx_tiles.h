@@ -186,6 +186,17 @@ __device__ __forceinline__ void store_four(const MxGemmArgs& a, int64_t bias0, i
   }
 }
 
+// Four neighbouring values at p + at, all inside and aligned for one load.
+template <bool kBf16>
+__device__ __forceinline__ f32x4 load_four(const void* p, int64_t at) {
+  if constexpr (kBf16) {
+    const u32x2 w = *(global_ptr<const u32x2>)((global_ptr<const uint16_t>)p + at);
+    return f32x4{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+  } else {
+    return *(global_ptr<const f32x4>)((global_ptr<const float>)p + at);
+  }
+}
+
 // Whether D's rows allow a store of four values at once.
 template <bool kBf16>
 __device__ __forceinline__ bool wide_rows(const MxGemmArgs& a) {

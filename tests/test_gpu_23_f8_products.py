@@ -135,6 +135,36 @@ def test_alpha_beta_bias(M, N, K, out):
     dense(M, N, K, out, alpha=0.0, beta=1.0)
 
 
+@pytest.mark.parametrize("out", ["BF16", "F32"])
+@pytest.mark.parametrize("M,N,K", [(40, 128, 256), (130, 256, 512), (300, 512, 256), (2200, 1024, 128), (130, 384, 17000)])
+def test_c_and_bias_at_every_alignment(M, N, K, out):
+    """Whole blocks of columns with C, bias and D aligned for wide accesses and each of them not."""
+    import torch
+    log("f8 alignment", M, N, K, out)
+    A, As, a = make(M, K, 1)
+    B, Bs, b = make(N, K, 2)
+    A, As, B, Bs = up(A), up(As), up(B), up(Bs)
+    g = np.random.default_rng(5)
+    t = torch_out(out)
+    c = torch.from_numpy(g.standard_normal((M, N)) * 10).to(t).cuda()
+    v = torch.from_numpy(g.standard_normal(N) * 10).to(t).cuda()
+    ws = workspace(M, N, f8.pitch(K))
+
+    def at(x, skew, pitch):
+        rows, cols = x.shape
+        w = torch.full((skew + rows * pitch,), -5.0, dtype=t, device="cuda")[skew:].as_strided((rows, cols), (pitch, 1))
+        w.copy_(x)
+        return w
+
+    for dc, dv, dd in ((0, 0, 0), (1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 1), (2, 2, 0)):
+        bias = at(v[None], dv, N)[0]
+        for beta in (0.0, 2.0):
+            for with_bias in (False, True):
+                D, C = at(torch.zeros_like(c), dd, N + dd), at(c, dc, N + dc)
+                dg.dist_gemm_f8_product(A, As, B, Bs, D, bias=bias if with_bias else None, C=C, beta=beta, alpha=0.5, workspace=ws)
+                check(f64(D), a, b, out, 0.5, beta, f64(c), f64(v) if with_bias else None)
+
+
 def test_without_beta_c_is_not_read():
     import torch
     A, As, a = make(70, 256, 1)
