@@ -107,7 +107,9 @@ __device__ __forceinline__ uint32_t row16_lane(uint32_t v) {
 // The squares' order: workgroup b runs on XCD b mod 8 and takes place b / 8 of
 // that XCD's contiguous share; the order goes down kBands bands of rows, then
 // one square to the right, so that the bytes of a line of scales (one per square,
-// of either tensor) meet in one L2.
+// of either tensor) meet in one L2.  Each group of bands starts at a column of
+// its own: where rows are a power of two apart, XCDs at the same columns of
+// different rows would share the memory's channels.
 constexpr uint32_t kXcds = 8, kBands = 8;
 struct Squares {
   uint32_t bands, across;
@@ -118,7 +120,9 @@ __device__ __forceinline__ bool square_of(const Squares& q, uint32_t block, uint
   const uint32_t w = x * each + min(x, more) + i, group = w / (kBands * q.across), in = w - group * kBands * q.across;
   const uint32_t high = min(kBands, q.bands - group * kBands);
   band = group * kBands + in % high;
-  kb = in / high;
+  const uint32_t from = ((group * 0x9E3779B1u >> 16) * q.across) >> 16;  // (across < 2^16, or any start will do)
+  kb = in / high + from % q.across;
+  kb -= kb >= q.across ? q.across : 0;
   return true;
 }
 

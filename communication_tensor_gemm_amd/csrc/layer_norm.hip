@@ -435,19 +435,21 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBack
   if constexpr (kSums) {
     // this workgroup's two rows of partial sums; several short rows' lanes are added through LDS
     float* const to = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-    __shared__ float sums[2][4][512];
+    __shared__ float sums[2][4 * 512 * V];  // of four waves' columns
     if (groups > 1) {
-      // only rows of at most 512 columns come several to a workgroup (one piece per lane)
+      const int of_group = 512 * V * W, first = wave / W * of_group;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sums[0][wave][8 * t + j] = dw[0][j];
-        sums[1][wave][8 * t + j] = db[0][j];
-      }
+      for (int c = 0; c < V; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sums[0][first + 8 * (c * span + t) + j] = dw[c][j];
+          sums[1][first + 8 * (c * span + t) + j] = db[c][j];
+        }
       __syncthreads();
       for (int i = threadIdx.x; i < 2 * a.cols; i += blockDim.x) {
         const int which = i >= a.cols, col = i - which * a.cols;
         float v = 0.0f;
-        for (int g = 0; g < groups; ++g) v += sums[which][g][col];
+        for (int g = 0; g < groups; ++g) v += sums[which][g * of_group + col];
         to[i] = v;
       }
       return;
@@ -525,13 +527,14 @@ __global__ __launch_bounds__(1024) void layer_norm_dweight_kernel(const float* p
   }
 }
 
-// One row per workgroup of W waves, or four rows of one wave each where a row
-// has at most 512 columns; as many workgroups as the chip holds at a time.
+// Workgroups of one row of W waves, or of 4 / W rows where W is less than four
+// (65536 x 1000 bf16 with dh: 128 us with one row of one wave to each, 95 with
+// four); as many workgroups as the chip holds at a time.
 static void backward_shape(int type, int64_t rows, int64_t cols, int* W, int* groups, int64_t* blocks) {
   const int d = static_cast<int>((cols + 7) / 8), pieces = type == PT_BF16 && d > 64 ? 2 : 1;
   *W = 1;
   while (*W < kMaxWaves && 64 * *W * pieces < d) *W *= 2;
-  *groups = cols <= 512 ? 4 : 1;
+  *groups = *W < 4 ? 4 / *W : 1;
   const int waves = *W * *groups, fit = waves >= 16 ? 1 : (waves >= 8 ? 2 : 4);
   const int64_t want = (rows + *groups - 1) / *groups, cap = 256 * fit;
   *blocks = want < cap ? want : cap;
