@@ -192,7 +192,18 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(LayerNormArgs a, int W
   }
 }
 
-// Waves of a row: the fewest that keep a lane's pieces at four, or, with too
+// How the rows are reached.  fp32 stays in the caches: a lane's 32 bytes are two
+// accesses to half of each line's bytes, and past the caches lines move twice
+// (norm 8192 x 8192 115 us, so 104; with residual 220 and 200; gradient from
+// the checkpoint with dh 178 and 163).
+template <int T>
+static int access_of(uint64_t misaligned, int64_t cols, int64_t bytes) {
+  if ((misaligned & 15) != 0 || cols % 8 != 0) return ANY;
+  return T == PT_F32 || bytes < kLastLevelCache ? ALIGNED : STREAM;
+}
+
+// Waves of a row: the fewest that keep a lane's pieces at two (8192 x 8192 bf16
+// into F8 with the checkpoint: 97 us; four pieces 102, one 116), or, with too
 // few rows to fill the chip, as many as have a piece each.
 static int row_waves(int64_t rows, int d) {
   const int per_lane = rows >= 2048 ? 2 : 1;
@@ -206,8 +217,9 @@ static void norm_v(const LayerNormArgs& a, int W, int access, hipStream_t st) {
   const int groups = W >= 4 ? 1 : 4 / W;
   const int64_t blocks = (a.rows + groups - 1) / groups;
   const dim3 grid(grid_x(blocks), grid_y(blocks)), block(64 * W * groups);
+  constexpr int kStream = T == PT_F32 ? ALIGNED : STREAM;
   if (access == STREAM)
-    hipLaunchKernelGGL((layer_norm_kernel<T, OUT, V, STREAM>), grid, block, 0, st, a, W);
+    hipLaunchKernelGGL((layer_norm_kernel<T, OUT, V, kStream>), grid, block, 0, st, a, W);
   else if (access == ALIGNED)
     hipLaunchKernelGGL((layer_norm_kernel<T, OUT, V, ALIGNED>), grid, block, 0, st, a, W);
   else
@@ -226,7 +238,7 @@ static void norm_t(const LayerNormArgs& a, hipStream_t st) {
   if (OUT == LO_SAME) m |= reinterpret_cast<uint64_t>(a.y) | static_cast<uint64_t>(a.ldy * es);
   if (OUT == LO_E4M3) m |= (reinterpret_cast<uint64_t>(a.y) | static_cast<uint64_t>(a.ldy)) << 1;  // 8-byte stores
   const int64_t bytes = a.rows * a.cols * ((a.residual ? 3 : 1) * es + (OUT == LO_SAME ? es : 1) + (a.kept ? 1 : 0));
-  const int access = (m & 15) != 0 || a.cols % 8 != 0 ? ANY : bytes < kLastLevelCache ? ALIGNED : STREAM;
+  const int access = access_of<T>(m, a.cols, bytes);
   if (v <= 1)
     norm_v<T, OUT, 1>(a, W, access, st);
   else if (v <= 2)
@@ -565,8 +577,9 @@ static void backward_v(const LayerNormBackwardArgs& a, int W, int groups, int64_
     else
       hipLaunchKernelGGL((layer_norm_columns_kernel<T, KEPT, ALIGNED>), grid, dim3(256), 0, st, a);
   }
+  constexpr int kStream = T == PT_F32 ? ALIGNED : STREAM;
   if (access == STREAM)
-    backward_launch<T, KEPT, V, STREAM>(a, W, groups, blocks, st);
+    backward_launch<T, KEPT, V, kStream>(a, W, groups, blocks, st);
   else if (access == ALIGNED)
     backward_launch<T, KEPT, V, ALIGNED>(a, W, groups, blocks, st);
   else
@@ -585,7 +598,7 @@ static hipError_t backward_t(const LayerNormBackwardArgs& a, hipStream_t st) {
   int64_t blocks;
   backward_shape(T, a.rows, a.cols, &W, &groups, &blocks);
   const int d = (a.cols + 7) / 8, v = (d + 64 * W - 1) / (64 * W);
-  const int access = (m & 15) != 0 || a.cols % 8 != 0 ? ANY : bytes < kLastLevelCache ? ALIGNED : STREAM;
+  const int access = access_of<T>(m, a.cols, bytes);
   if (blocks == 0)
     ;  // no rows: the second kernel writes zeros
   else if (v <= 1)
