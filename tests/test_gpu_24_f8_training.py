@@ -129,6 +129,26 @@ def test_captured():
         assert all(torch.equal(p, q) for p, q in zip(results(), want))
 
 
+def test_two_layers_at_once():
+    """Two layers' steps on two streams, each with its own tensors and workspaces, equal the steps one after the other."""
+    import torch
+    made = [layer(300, 520, 392), layer(257, 384, 640)]
+    want = []
+    for L, x, r, dy, dh in made:
+        y, dx = L.forward(x, r), L.backward(dy, dh)
+        want.append([t.clone() for t in (y, dx, L.dweight, L.dnorm_weight, L.dnorm_bias)])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(5):
+        for s, (L, x, r, dy, dh) in zip(streams, made):
+            with torch.cuda.stream(s):
+                L.forward(x, r)
+                L.backward(dy, dh)
+    torch.cuda.synchronize()
+    for w, (L, *_) in zip(want, made):
+        assert all(torch.equal(p, q) for p, q in zip(w, (L.y, L.dx, L.dweight, L.dnorm_weight, L.dnorm_bias)))
+
+
 def test_weight_gradients_accumulate():
     """A second batch's gradient on top of the first, in fp32, with beta = 1."""
     import torch
