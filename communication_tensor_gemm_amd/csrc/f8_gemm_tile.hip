@@ -1,5 +1,29 @@
-// F8 product on square tiles, for many rows of A (mx_tile_loop.h has the main
-// loop).
+// F8 product on tiles, for many rows of A (mx_tile_loop.h has the main loop).
+//
+//   D_ij = alpha sum_b 2^(Xa_ib + Xb_jb) sum_k a_ik b_jk + beta C_ij + bias_j,
+// b the blocks of 128 of K, k within one.  The powers of two are operands of the
+// MFMA, so a block's scale costs no instruction per output; scales that were
+// no powers of two would take a multiply-add per block and output, which the
+// accumulators, in AGPRs, cannot have.
+//
+// Rates.  16384 x 13312 x 16384: 2550 .. 2690 us from box to box, 2.7 .. 2.8
+// PFLOP/s, 78 to 82% of what MFMAs alone reach on random data (3.4, bound by
+// power); the MFMA pipe is busy 74% of the cycles, waits take 17%.  8192 x 3584 x
+// 8192 197 .. 205 us: 448 tiles on 256 CUs, two rounds of which the second is 3/4
+// full.  LDS is the next bound: a slab of a 256 x 256 tile writes 64 KiB into it
+// (64 bytes a cycle) and reads 128 (128 a cycle), as many cycles as its MFMAs.
+// C or a bias beside whole columns: four columns per access (into fp32 with C
+// 238 us, by single elements 280; without C 233).
+//
+// Tiles of 64 x 128 (four stages, one workgroup per CU) are for up to one of
+// them per CU: 200 x 8192 x 3584 15 us, 0.38 per slab of 24 KiB; tiles of 128 x 128
+// 22, 0.62 per slab of 32 KiB on half of the CUs.  Three, four or six stages
+// measure the same (15.6, 15.6, 16.5), two groups of four waves 17.3: a CU moves
+// about 62 KB/us of slabs into LDS and twice that out of it in all of these forms.
+//
+// Precision: as the MX products' E4M3 (mx_gemm_tile.hip): eight consecutive
+// products are added to 2^-13 of the largest one's power of two, 2e-5 of the
+// result's rms, the rest in fp32.
 #include "f8_common.h"
 #include "mx_tile_loop.h"
 
@@ -22,6 +46,7 @@ static hipError_t tile_t(const MxGemmArgs& a, hipStream_t st) {
   const int64_t grid = ((T < most ? T : most) + kXcds - 1) / kXcds * kXcds;
   const dim3 wgs(static_cast<unsigned>(grid));
   if constexpr (NBM == 2) {
+    // two groups of waves / one: 1024 x 4096 x 16384 88 / 93 us, 2000 x 2000 x 8192 42 / 48, 300 x 10000 x 16384 97 / 113
     if (T <= a.cus && a.K > 4096) {
       hipLaunchKernelGGL((f8_gemm_tile_kernel<kBf16, NBM, NBN, 2, false>), wgs, dim3(512), 0, st, a);
       return hipGetLastError();

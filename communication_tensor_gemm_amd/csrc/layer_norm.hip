@@ -7,7 +7,13 @@
 //   dx = s (g - mean(g) - n mean(g n)) + dh,   dw = sum dy n,  db = sum dy
 // All sums are fp32.  Both directions are bound by memory: every input is
 // read once and every output written once, the row staying in registers
-// between its sums and its use.
+// between its sums and its use.  8192 x 8192 bf16 with residual into F8 with the
+// checkpoint: 95 us, 5.7 TB/s (a copy: 6.2); 4 x 16384 into F8: 5.9 us, the latency
+// of loads, two sums over 16 waves and a store; the gradient of 8192 x 8192 bf16
+// from the checkpoint with dh: 91 us, 5.2 TB/s (its second kernel 6.4 of them), from
+// the stream 100; of 1021 x 5123 fp32 19.7 us, two dependent launches (16.7 and
+// 3.9).  Rows of few columns are bound by their waves: a row has one of its own,
+// 262144 x 128 bf16 takes 90 us, its gradient 75.
 //
 // The variance is of the differences from a mean, never a difference of two
 // sums: each wave sums its part of the row and the squares around its own
@@ -265,8 +271,9 @@ static void norm_out(int out, const LayerNormArgs& a, hipStream_t st) {
 // those rows.  No atomics: the order of every sum is fixed.  The next row's
 // loads are in flight while the current row's sums cross the waves, where the
 // registers allow it.  Rows of more than 16384 columns have no registers for
-// the columns' sums: there the first kernel leaves them to a kernel that walks
-// down the columns.
+// the columns' sums: there a kernel of its own walks down the columns first
+// (4096 x 32768 bf16 from the checkpoint with dh 272 us, 2048 x 32768 fp32 332: half
+// of the bytes are read twice).
 
 // Eight elements of a row's dy and n (or h), as loaded.
 template <int T, bool KEPT>

@@ -1,4 +1,4 @@
-// Products on square tiles, for many rows of A: the main loop that the MX
+// Products on tiles, for many rows of A: the main loop that the MX
 // products (mx_gemm_tile.hip) and the F8 products (f8_gemm_tile.hip) share.
 //
 // Tiling.  A workgroup of four waves, 2 x 2, computes a tile of 64 NBM x 64
@@ -8,16 +8,17 @@
 // columns of a row of D.
 //
 // K is walked in slabs of 128 bytes per row of A: 256 elements of E2M1 (128
-// bytes per row of B too) or 128 of E4M3 (64 bytes per row of B), each in two
-// halves.  Slabs go from memory straight into LDS (buffer_load_dwordx4 ...
+// bytes per row of B too) or 128 of E4M3 (64 bytes per row of an E2M1 B, 128 of an
+// E4M3 B), each in two halves.  Slabs go from memory straight into LDS (buffer_load_dwordx4 ...
 // lds, 1 KiB per wave instruction, whole lines of 128 bytes where the rows
 // allow it: slabs of 64 bytes per row, twice as many of them, measured 13%
-// slower), two stages of E2M1 or three of E4M3; the scales in chunks of 512
-// elements (16 bytes per row), two buffers.  While half a slab is multiplied
+// slower), two stages of E2M1 or of E4M3 by E4M3 (four of tiles of 64 x 128) or
+// three of E4M3 by E2M1; the scales in chunks of 16 bytes per row (512 elements,
+// or 2048 of F8 operands), two buffers.  While half a slab is multiplied
 // from one set of registers, the next half is read from LDS into the other.
 // One barrier per slab, between its halves, says that every wave has read
-// the second half, which frees the slab's stage for the loads of the slab two
-// (E4M3: three) further on, and that the next slab has landed.  MFMAs, reads
+// the second half, which frees the slab's stage for the loads of the slab as
+// many further on as there are stages, and that the next slab has landed.  MFMAs, reads
 // and loads alternate in a fixed order (scheduling barriers keep it).  The
 // scales' loads touch a line per lane, so they are placed in the half without
 // other loads.
@@ -44,7 +45,8 @@
 // elements 16 h .. + 15 and 32 + 16 h .. + 15 of 64.  Its scale is that of
 // block h of the 64, in both cases: of a dword of scales (four blocks, 128
 // elements), byte h for the first 64 and 2 + h for the second, so the dword is
-// shifted by h bytes once and op_sel takes bytes 0 and 2.
+// shifted by h bytes once and op_sel takes bytes 0 and 2.  An F8 operand's slab
+// is one block of 128: its byte is read by itself and serves all four.
 //
 // LDS layout.  128-byte rows: blocks of 8 rows (1 KiB), half row s at + 512 s,
 // row r at + 64 (r % 8), 16-byte piece q of the half at + 16 (q ^ f(r)), f(r) =
