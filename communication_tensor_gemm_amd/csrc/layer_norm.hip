@@ -31,17 +31,21 @@ namespace f8 {
 
 constexpr int kMaxWaves = 16;
 
-// Sum over the wave's lanes, in all of them: within 16 lanes by DPP, over the four rows by lane swaps.
+// Sum over the wave's lanes (or each 16 or 32 of them), in all of them: within 16 lanes by DPP, over the four rows by
+// lane swaps.
+template <int LANES = 64>
 __device__ __forceinline__ float wave_total(float v) {
   auto add = [](float x, int y) { return x + __builtin_bit_cast(float, y); };
   v = add(v, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xf, 0xf, true));
   v = add(v, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4E, 0xf, 0xf, true));
   v = add(v, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x141, 0xf, 0xf, true));
   v = add(v, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x140, 0xf, 0xf, true));
+  if constexpr (LANES == 16) return v;
   const uint32_t u = __builtin_bit_cast(uint32_t, v);
   const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
   const uint32_t a0 = a[0], a1 = a[1];
   v = __builtin_bit_cast(float, a0) + __builtin_bit_cast(float, a1);
+  if constexpr (LANES == 32) return v;
   const uint32_t x = __builtin_bit_cast(uint32_t, v);
   const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
   const uint32_t b0 = b[0], b1 = b[1];
@@ -62,15 +66,19 @@ __device__ __forceinline__ void store_bytes(uint8_t* y, u32x2 q, int n) {
   }
 }
 
-// grid: the rows over workgroups of several rows (W waves each), along x and, past kGridX, y
-template <int T, int OUT, int V, int A>
+// grid: the rows over workgroups of several rows (W waves each, or LANES lanes of
+// one), along x and, past kGridX, y
+template <int T, int OUT, int V, int A, int LANES>
 __global__ __launch_bounds__(1024) void layer_norm_kernel(LayerNormArgs a, int W) {
   constexpr int kShared = A == ANY ? ANY : ALIGNED;  // what every row reads
   __shared__ f32x2 parts[kMaxWaves];
-  // (a wave's row is one: kept in scalar registers, with its addresses)
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), groups = (blockDim.x >> 6) / W, part = wave % W;
-  const int t = part * 64 + (threadIdx.x & 63), span = 64 * W;
-  const int64_t row = (static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x) * groups + wave / W;
+  constexpr bool kWhole = LANES == 64;  // whole waves to a row
+  // (a whole wave's row is one: kept in scalar registers, with its addresses)
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = kWhole ? wave % W : 0;
+  const int groups = kWhole ? (blockDim.x >> 6) / W : blockDim.x / LANES;
+  const int t = kWhole ? part * 64 + (threadIdx.x & 63) : threadIdx.x % LANES, span = kWhole ? 64 * W : LANES;
+  const int64_t row = (static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x) * groups +
+                      (kWhole ? wave / W : static_cast<int>(threadIdx.x) / LANES);
   const bool live = row < a.rows;
   const int d = (a.cols + 7) / 8;
   Raw8<T> x[V];
@@ -112,7 +120,7 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(LayerNormArgs a, int W
   // elements of piece i inside the row
   auto inside = [&](int i) { return min(max(a.cols - 8 * i, 0), 8); };
   float sum = 0.0f;
-  int count = 0;  // elements of this wave
+  int count = kWhole ? 0 : a.cols;  // elements of this wave, or of the row
 #pragma unroll
   for (int c = 0; c < V; ++c) {
     float f[8];
@@ -121,9 +129,9 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(LayerNormArgs a, int W
 #pragma unroll
     for (int j = 0; j < 8; ++j) s8 += f[j];  // (zeros past the end)
     sum += s8;
-    count += min(max(a.cols - 8 * (c * span + part * 64), 0), 512);
+    if constexpr (kWhole) count += min(max(a.cols - 8 * (c * span + part * 64), 0), 512);
   }
-  float mean = wave_total(sum) / static_cast<float>(max(count, 1));
+  float mean = wave_total<LANES>(sum) / static_cast<float>(max(count, 1));
   float m2 = 0.0f;
 #pragma unroll
   for (int c = 0; c < V; ++c) {
@@ -138,8 +146,8 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(LayerNormArgs a, int W
     }
     m2 += s8;
   }
-  m2 = wave_total(m2);
-  if (W > 1) {
+  m2 = wave_total<LANES>(m2);
+  if (kWhole && W > 1) {
     if ((threadIdx.x & 63) == 0) parts[wave] = f32x2{mean, m2};
     __syncthreads();
     // a part to a lane (a loop over the parts would wait for LDS once per part)
@@ -218,18 +226,18 @@ static int row_waves(int64_t rows, int d) {
   return W;
 }
 
-template <int T, int OUT, int V>
+template <int T, int OUT, int V, int LANES = 64>
 static void norm_v(const LayerNormArgs& a, int W, int access, hipStream_t st) {
-  const int groups = W >= 4 ? 1 : 4 / W;
+  const int groups = LANES < 64 ? 256 / LANES : W >= 4 ? 1 : 4 / W;
   const int64_t blocks = (a.rows + groups - 1) / groups;
-  const dim3 grid(grid_x(blocks), grid_y(blocks)), block(64 * W * groups);
+  const dim3 grid(grid_x(blocks), grid_y(blocks)), block(LANES < 64 ? 256 : 64 * W * groups);
   constexpr int kStream = T == PT_F32 ? ALIGNED : STREAM;
   if (access == STREAM)
-    hipLaunchKernelGGL((layer_norm_kernel<T, OUT, V, kStream>), grid, block, 0, st, a, W);
+    hipLaunchKernelGGL((layer_norm_kernel<T, OUT, V, kStream, LANES>), grid, block, 0, st, a, W);
   else if (access == ALIGNED)
-    hipLaunchKernelGGL((layer_norm_kernel<T, OUT, V, ALIGNED>), grid, block, 0, st, a, W);
+    hipLaunchKernelGGL((layer_norm_kernel<T, OUT, V, ALIGNED, LANES>), grid, block, 0, st, a, W);
   else
-    hipLaunchKernelGGL((layer_norm_kernel<T, OUT, V, ANY>), grid, block, 0, st, a, W);
+    hipLaunchKernelGGL((layer_norm_kernel<T, OUT, V, ANY, LANES>), grid, block, 0, st, a, W);
 }
 
 template <int T, int OUT>
@@ -245,7 +253,12 @@ static void norm_t(const LayerNormArgs& a, hipStream_t st) {
   if (OUT == LO_E4M3) m |= (reinterpret_cast<uint64_t>(a.y) | static_cast<uint64_t>(a.ldy)) << 1;  // 8-byte stores
   const int64_t bytes = a.rows * a.cols * ((a.residual ? 3 : 1) * es + (OUT == LO_SAME ? es : 1) + (a.kept ? 1 : 0));
   const int access = access_of<T>(m, a.cols, bytes);
-  if (v <= 1)
+  // (few columns: four or two rows to a wave)
+  if (d <= 16)
+    norm_v<T, OUT, 1, 16>(a, 1, access, st);
+  else if (d <= 32)
+    norm_v<T, OUT, 1, 32>(a, 1, access, st);
+  else if (v <= 1)
     norm_v<T, OUT, 1>(a, W, access, st);
   else if (v <= 2)
     norm_v<T, OUT, 2>(a, W, access, st);

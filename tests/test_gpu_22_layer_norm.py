@@ -131,7 +131,8 @@ def run_forward(rows, cols, typ, out, residual, seed, kept=True, bias=True, pitc
 
 
 FORWARD_SIZES = [(1, 1), (1, 32), (2, 7), (5, 64), (3, 500), (4, 512), (9, 520), (3, 1000), (2, 2048), (5, 5123), (2, 8192),
-                 (3, 16384), (2, 20000), (2, 32768), (2100, 96), (2049, 1025), (2050, 4104)]
+                 (3, 16384), (2, 20000), (2, 32768), (2100, 96), (2049, 1025), (2050, 4104), (70, 128), (131, 129), (67, 250), (1, 256),
+                 (300, 3)]
 
 
 @pytest.mark.parametrize("residual", [False, True])
