@@ -12,8 +12,7 @@
 // of loads, two sums over 16 waves and a store; the gradient of 8192 x 8192 bf16
 // from the checkpoint with dh: 91 us, 5.2 TB/s (its second kernel 6.4 of them), from
 // the stream 100; of 1021 x 5123 fp32 19.7 us, two dependent launches (16.7 and
-// 3.9).  Rows of few columns are bound by their waves: a row has one of its own,
-// 262144 x 128 bf16 takes 90 us, its gradient 75.
+// 3.9).
 //
 // The variance is of the differences from a mean, never a difference of two
 // sums: each wave sums its part of the row and the squares around its own
@@ -23,7 +22,9 @@
 //
 // A row belongs to W waves (W = 1 .. 16), each lane holding V pieces of eight
 // consecutive elements, piece c of lane t of the row at 8 (c * 64 W + t): wide
-// loads, and an F8 block of 128 is 16 adjacent lanes.
+// loads, and an F8 block of 128 is 16 adjacent lanes.  Rows of up to 128 and 256
+// columns have 16 and 32 lanes, four or two rows to a wave (262144 x 128 bf16: 25 us,
+// with a wave to a row 90; its gradient 41 and 75).
 #include "f8_common.h"
 
 namespace dg {
@@ -330,15 +331,19 @@ struct Pair {
   }
 };
 
-template <int T, bool KEPT, int V, int A>
+// (LANES: of a row, as in the forward kernel)
+template <int T, bool KEPT, int V, int A, int LANES>
 __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBackwardArgs a, int W) {
   constexpr int kShared = A == ANY ? ANY : ALIGNED;
   constexpr bool kSums = V <= 2, kAhead = V == 1 || (V == 2 && T == PT_BF16);
   constexpr int N = kAhead ? V : 1;
   __shared__ f32x2 red[2][kMaxWaves];
-  // (a wave's row is one: kept in scalar registers, with its addresses)
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), groups = (blockDim.x >> 6) / W, part = wave % W;
-  const int t = part * 64 + (threadIdx.x & 63), span = 64 * W;
+  constexpr bool kWhole = LANES == 64;
+  // (a whole wave's row is one: kept in scalar registers, with its addresses)
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = kWhole ? wave % W : 0;
+  const int groups = kWhole ? (blockDim.x >> 6) / W : blockDim.x / LANES;
+  const int group = kWhole ? wave / W : static_cast<int>(threadIdx.x) / LANES;
+  const int t = kWhole ? part * 64 + (threadIdx.x & 63) : threadIdx.x % LANES, span = kWhole ? 64 * W : LANES;
   const int d = (a.cols + 7) / 8;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const float inv_n = 1.0f / static_cast<float>(a.cols);
@@ -358,7 +363,7 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBack
     for (int c = 0; c < V; ++c) weight(c, wr[c]);
   }
   // all groups of the workgroup make the same number of turns (they share the barrier)
-  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + wave / W;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
   const int64_t turns = (a.rows - static_cast<int64_t>(blockIdx.x) * groups + step - 1) / step;
   Pair<T, KEPT> in[V], ahead[N];
   Raw8<T> dh[kSums ? V : 1];
@@ -427,9 +432,9 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBack
       sg += g8;
       sgn += gn8;
     }
-    sg = wave_total(sg);
-    sgn = wave_total(sgn);
-    if (W > 1) {
+    sg = wave_total<LANES>(sg);
+    sgn = wave_total<LANES>(sgn);
+    if (kWhole && W > 1) {
       // two sets of slots: a wave may be one turn ahead of another's reads
       if ((threadIdx.x & 63) == 0) red[k & 1][wave] = f32x2{sg, sgn};
       __syncthreads();
@@ -469,7 +474,7 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(LayerNormBack
     float* const to = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
     __shared__ float sums[2][4 * 512 * V];  // of four waves' columns
     if (groups > 1) {
-      const int of_group = 512 * V * W, first = wave / W * of_group;
+      const int of_group = 8 * V * span, first = group * of_group;
 #pragma unroll
       for (int c = 0; c < V; ++c)
 #pragma unroll
@@ -562,12 +567,13 @@ __global__ __launch_bounds__(1024) void layer_norm_dweight_kernel(const float* p
 // Workgroups of one row of W waves, or of 4 / W rows where W is less than four
 // (65536 x 1000 bf16 with dh: 128 us with one row of one wave to each, 95 with
 // four); as many workgroups as the chip holds at a time.
+static int row_lanes(int64_t cols) { return cols <= 128 ? 16 : cols <= 256 ? 32 : 64; }
 static void backward_shape(int type, int64_t rows, int64_t cols, int* W, int* groups, int64_t* blocks) {
   const int d = static_cast<int>((cols + 7) / 8), pieces = type == PT_BF16 && d > 64 ? 2 : 1;
   *W = 1;
   while (*W < kMaxWaves && 64 * *W * pieces < d) *W *= 2;
-  *groups = *W < 4 ? 4 / *W : 1;
-  const int waves = *W * *groups, fit = waves >= 16 ? 1 : (waves >= 8 ? 2 : 4);
+  *groups = cols <= 256 ? 256 / row_lanes(cols) : *W < 4 ? 4 / *W : 1;
+  const int waves = cols <= 256 ? 4 : *W * *groups, fit = waves >= 16 ? 1 : (waves >= 8 ? 2 : 4);
   const int64_t want = (rows + *groups - 1) / *groups, cap = 256 * fit;
   *blocks = want < cap ? want : cap;
 }
@@ -582,8 +588,17 @@ static int64_t partial_rows(int64_t rows, int64_t cols, int64_t blocks) {
 
 template <int T, bool KEPT, int V, int A>
 static void backward_launch(const LayerNormBackwardArgs& a, int W, int groups, int64_t blocks, hipStream_t st) {
-  hipLaunchKernelGGL((layer_norm_backward_kernel<T, KEPT, V, A>), dim3(static_cast<unsigned>(blocks)),
-                     dim3(64 * W * groups), 0, st, a, W);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if constexpr (V == 1) {
+    // (few columns: four or two rows to a wave)
+    const int lanes = row_lanes(a.cols);
+    if (lanes == 16)
+      hipLaunchKernelGGL((layer_norm_backward_kernel<T, KEPT, V, A, 16>), grid, dim3(256), 0, st, a, W);
+    if (lanes == 32)
+      hipLaunchKernelGGL((layer_norm_backward_kernel<T, KEPT, V, A, 32>), grid, dim3(256), 0, st, a, W);
+    if (lanes < 64) return;
+  }
+  hipLaunchKernelGGL((layer_norm_backward_kernel<T, KEPT, V, A, 64>), grid, dim3(64 * W * groups), 0, st, a, W);
 }
 
 template <int T, bool KEPT, int V>

@@ -243,7 +243,8 @@ def run_backward(rows, cols, typ, kept, with_dh, seed, pitch=None, skew=0, in_pl
 
 
 BACKWARD_SIZES = [(1, 1), (1, 8), (3, 7), (5, 64), (4, 512), (1030, 500), (9, 520), (600, 1000), (3, 5123), (700, 8192),
-                  (3, 8200), (530, 16384), (3, 16385), (3, 20000), (520, 32768)]
+                  (3, 8200), (530, 16384), (3, 16385), (3, 20000), (520, 32768), (70, 128), (1031, 129), (5000, 250), (20000, 100),
+                  (300, 3)]
 
 
 @pytest.mark.parametrize("kept", [False, True])
