@@ -19,12 +19,12 @@
 // quarters of the wave hold the chunk's first block, the two upper ones its
 // second, and quarter q passes the scale of block q % 2.
 //
-// A comes through LDS where its rows fit there (kLds), copied once and densely;
+// A comes through LDS where its rows fit and K is long (kLds), copied once and densely;
 // else from L2 where it is used, in the same way as B.
 //
 // 1 x 13312 x 16384 (220 MB): 38.5 us, 5.7 TB/s, launch and the latency of the
 // first loads included (a copy: 6.2).  More rows of that width, whose A is read
-// again by every workgroup: 8 52 us, 16 55, 32 62; 1 x 8192 x 3584 8.3, 16 9.5.
+// again by every workgroup: 4 45 us, 8 52, 16 54, 32 62; 1 x 8192 x 1024 4.2, 16 4.2.
 #include "f8_common.h"
 #include "mx_tiles.h"
 
@@ -33,7 +33,8 @@ namespace f8 {
 
 constexpr int kChunk = 256;  // elements of K per step of a wave
 constexpr int kWaves = 8;
-constexpr int kLdsA = 48 * 1024;       // bytes of A, its scales and their padding in LDS
+// bytes of A, its scales and their padding in LDS: three workgroups to a CU, or two
+constexpr int kLdsA = 48 * 1024, kMoreLdsA = 78 * 1024;
 constexpr int kPadA = 64, kPadS = 16;  // between rows: the 16 rows of a read on distinct banks
 
 // LDS bytes of `rows` rows of A and their scales
@@ -64,11 +65,13 @@ __device__ __forceinline__ void transpose_quads(i32x4 (&v)[4], bool odd, bool hi
   }
 }
 
-template <int MB, int NB, bool kBf16, bool kLds>
+// kLdsBytes: of A in LDS; 0: A from memory
+template <int MB, int NB, bool kBf16, int kLdsBytes>
 __global__ __launch_bounds__(64 * kWaves) void f8_gemm_rows_kernel(MxGemmArgs a, int step) {  // step: columns of a workgroup
+  constexpr bool kLds = kLdsBytes > 0;
   constexpr int kAhead = NB == 1 ? 2 : 1;  // chunks asked for before they are multiplied
   constexpr int kSums = kWaves / 2 * MB * NB * 64 * 16;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds && kLdsA > kSums ? kLdsA : kSums];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLdsBytes > kSums ? kLdsBytes : kSums];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int32_t n_tiles = tile_count(a.N, step);
@@ -228,7 +231,7 @@ __global__ __launch_bounds__(64 * kWaves) void f8_gemm_rows_kernel(MxGemmArgs a,
   }
 }
 
-template <int MB, int NB, bool kLds>
+template <int MB, int NB, int kLdsBytes>
 static hipError_t rows_lds_t(const MxGemmArgs& a, hipStream_t st) {
   const int64_t tiles = tile_count(a.M, 16 * MB);
   const int step = rows_step(a.N, tiles, 16 * NB, a.cus);
@@ -236,20 +239,27 @@ static hipError_t rows_lds_t(const MxGemmArgs& a, hipStream_t st) {
   if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
   const dim3 grid(grid_x(blocks), grid_y(blocks)), block(64 * kWaves);
   if (a.out_bf16)
-    hipLaunchKernelGGL((f8_gemm_rows_kernel<MB, NB, true, kLds>), grid, block, 0, st, a, step);
+    hipLaunchKernelGGL((f8_gemm_rows_kernel<MB, NB, true, kLdsBytes>), grid, block, 0, st, a, step);
   else
-    hipLaunchKernelGGL((f8_gemm_rows_kernel<MB, NB, false, kLds>), grid, block, 0, st, a, step);
+    hipLaunchKernelGGL((f8_gemm_rows_kernel<MB, NB, false, kLdsBytes>), grid, block, 0, st, a, step);
   return hipGetLastError();
 }
 
-// Rows that fit into LDS leave a wave little else to load than B: 16 columns,
-// in two chunks ahead.  More of them: 32 columns, for half the reads of A (as
-// the MX products' kernel for few rows, where both were measured).
+// 32 columns to a workgroup, for half the reads of A; but up to 16 rows with more
+// than a chunk of K to each wave have A in LDS where it fits, and then 16 columns,
+// in two chunks ahead (with / without: 1 x 8192 x 4096 9.1 us / 11.4, 8 x 8192 x
+// 3584 9.1 / 9.4; 1 x 8192 x 2048 6.6 / 6.4, 16 x 8192 x 1024 5.6 / 4.2, 32 x 8192 x
+// 1024 7.2 / 5.2).  A long K is worth more LDS at two workgroups per CU instead of
+// three: 4 x 13312 x 16384 48 -> 42 us, 8 x 8192 x 8192 19 -> 14; a shorter one not
+// (16 x 13312 x 4608 15 and 17).
 template <int MB>
 static hipError_t rows_t(const MxGemmArgs& a, hipStream_t st) {
-  const int64_t rows = a.M < 16 * MB ? a.M : 16 * MB;
-  if (lds_a_bytes(rows, a.K) <= kLdsA) return rows_lds_t<MB, 1, true>(a, st);
-  return rows_lds_t<MB, 2, false>(a, st);
+  if constexpr (MB == 1) {
+    const int64_t bytes = lds_a_bytes(a.M < 16 ? a.M : 16, a.K);
+    if (bytes <= kLdsA && a.K > kChunk * kWaves) return rows_lds_t<1, 1, kLdsA>(a, st);
+    if (bytes <= kMoreLdsA && a.K >= 8192) return rows_lds_t<1, 1, kMoreLdsA>(a, st);
+  }
+  return rows_lds_t<MB, 2, 0>(a, st);
 }
 
 }  // namespace f8
@@ -258,7 +268,7 @@ hipError_t launch_f8_gemm(const MxGemmArgs& a, float* work, hipStream_t st) {
   if (a.M == 0) return hipSuccess;
   const F8Choice c = f8_choice(a.M, a.N, a.K, a.cus);
   if (c.rows == 16) return f8::rows_t<1>(a, st);
-  if (c.rows == 32) return a.M <= 32 ? f8::rows_t<2>(a, st) : f8::rows_lds_t<2, 2, false>(a, st);
+  if (c.rows == 32) return f8::rows_t<2>(a, st);
   if (c.rows == 64) return f8::rows_t<4>(a, st);
   if (c.parts > 1) return launch_f8_gemm_split(a, c.parts, work, f8_split_pitch(a.N), st);
   return launch_f8_gemm_tile(c.size, a, st);

@@ -83,7 +83,7 @@ def dense(M, N, K, out, seed=1, alpha=1.0, beta=0.0, with_bias=False, pitch=None
     return f64(D), a, b
 
 
-SIZES = [(1, 1, 1), (1, 16, 128), (3, 5, 96), (16, 48, 512), (17, 33, 544), (1, 272, 4096), (31, 100, 992), (33, 64, 1536),
+SIZES = [(1, 1, 1), (1, 16, 128), (3, 5, 96), (16, 48, 512), (17, 33, 544), (1, 272, 4096), (4, 60, 16384), (15, 70, 4096), (31, 90, 2048), (60, 200, 1100), (31, 100, 992), (33, 64, 1536),
          (2, 100, 16384), (5, 40, 20000), (64, 130, 2080), (65, 257, 160), (100, 300, 1024), (129, 128, 3584), (200, 520, 608),
          (256, 256, 256), (300, 700, 1120), (513, 260, 512), (700, 1030, 2048), (150, 500, 6000), (520, 530, 4224), (140, 900, 128),
          # K in parts
