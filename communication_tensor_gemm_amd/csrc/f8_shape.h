@@ -25,7 +25,8 @@ struct F8Choice {
 // Up to 32 rows stream the weights.  From 33 to 64 rows, tiles of 64 x 128 take
 // over where they occupy 3/8 of the CUs (rows / tiles: 64 x 8192 x 3584 13.8 /
 // 14.1, 48 x 13312 x 16384 77 / 70, 64 x 13312 x 16384 82 / 71; 32 x 13312 x 16384
-// 61 / 68).
+// 61 / 68).  Past one round they always do: all their rounds together are more than
+// half full.
 //
 // Up to one 64 x 128 tile per CU, the least of three estimates: those tiles (5
 // + 0.35 per slab of 128 elements; tiles of 128 x 128, of which half as many run,
@@ -57,7 +58,7 @@ inline F8Choice f8_choice(int64_t M, int64_t N, int64_t K, int cus) {
     if (M <= 64) return 8 * low >= 3 * cus ? F8Choice{0, 64, 1} : F8Choice{64, 0, 1};
     return rows < whole ? F8Choice{32, 0, 1} : F8Choice{0, 64, 1};
   }
-  if (M <= 64) return 8 * low >= 3 * rounds(low) * cus ? F8Choice{0, 64, 1} : F8Choice{64, 0, 1};
+  if (M <= 64) return {0, 64, 1};
   return {0, 3 * rounds(tiles(256, 256)) <= rounds(tiles(128, 128)) ? 256 : 128, 1};
 }
 

@@ -59,3 +59,62 @@ def test_every_choice_over_the_range(tmp_path):
                     os.path.join(ROOT, "communication_tensor_gemm_amd", "csrc"), str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+CHOICES = r"""
+#include <stdio.h>
+#include <initializer_list>
+#include "f8_shape.h"
+int main() {
+  // of the kernels for few rows by their rows, of the tiles by size and whether K is in parts
+  long rows[3] = {0, 0, 0}, whole[3] = {0, 0, 0}, parts = 0, few_many = 0, other = 0;
+  for (int cus : {256, 304, 64})
+    for (int64_t M = 1; M <= 16384; M = M < 130 ? M + 1 : M * 5 / 4)
+      for (int64_t N = 1; N <= 70000; N = N < 20 ? N + 3 : N * 6 / 5)
+        for (int64_t K = 128; K <= 65536; K = K * 5 / 384 * 128 + 128) {
+          const dg::F8Choice c = dg::f8_choice(M, N, K, cus);
+          if (c.rows) ++(c.rows == 16 ? rows[0] : c.rows == 32 ? rows[1] : c.rows == 64 ? rows[2] : other);
+          else if (c.parts > 1) ++parts;
+          else ++(c.size == 64 ? whole[0] : c.size == 128 ? whole[1] : whole[2]);
+          // more 64 x 128 tiles than CUs: tiles for every M past 32
+          if (M > 32 && (M + 63) / 64 * ((N + 127) / 128) > cus) {
+            ++few_many;
+            other += c.rows != 0 || (M <= 64 && c.size != 64);
+          }
+        }
+  printf("rows %ld %ld %ld whole %ld %ld %ld parts %ld many %ld other %ld\n", rows[0], rows[1], rows[2], whole[0], whole[1], whole[2],
+         parts, few_many, other);
+  return !(rows[0] && rows[1] && rows[2] && whole[0] && whole[1] && whole[2] && parts && few_many && !other);
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_every_kernel_has_sizes(tmp_path):
+    """Each size of the kernel for few rows, each tile and K in parts is taken for some sizes."""
+    src, exe = tmp_path / "choices.cpp", tmp_path / "choices"
+    src.write_text(CHOICES)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Werror", "-I",
+                    os.path.join(ROOT, "communication_tensor_gemm_amd", "csrc"), str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+
+
+@pytest.mark.skipif(shutil.which("g++") is None or shutil.which("gcov") is None, reason="g++ or gcov not available")
+def test_no_part_of_the_choice_is_dead(tmp_path):
+    """Every branch of f8_choice goes both ways over the sizes above."""
+    (tmp_path / "choices.cpp").write_text(CHOICES)
+    header = os.path.join(ROOT, "communication_tensor_gemm_amd", "csrc")
+    subprocess.run(["g++", "-O0", "-std=c++17", "--coverage", "-I", header, "choices.cpp", "-o", "choices"], check=True, cwd=tmp_path)
+    subprocess.run(["./choices"], check=True, cwd=tmp_path, capture_output=True)
+    out = subprocess.run(["gcov", "-b", "-c", "-t", "choices.gcda"], check=True, cwd=tmp_path, capture_output=True, text=True).stdout
+    body = out[out.index("inline F8Choice f8_choice"):out.index("inline int64_t f8_gemm_workspace")]
+    dead, line = [], ""
+    for l in body.splitlines():
+        if l.lstrip().startswith("branch"):
+            # (a branch of an exception's clean-up is not one of the choice)
+            if "(throw)" not in l and ("never" in l or l.split()[3] == "0"):
+                dead.append(line)
+        elif ":" in l:
+            line = l
+    assert not dead, dead
