@@ -133,3 +133,14 @@ def check_sampled(w, x, D, rows, cols, schedule=None, TP=None, bias=None):
     assert ok, f"{w.name}: sampled max normalised error {mx}"
     assert tight, f"{w.name}: sampled tight bar failed (max err {mx})"
     return mx
+
+
+def within(got, ref, tol):
+    """Whether every value of `got` is within `tol` of `ref`, and the same where `ref` is an infinity or a NaN.  (A test of
+    `not any(|got - ref| > tol)` alone would pass a NaN.)"""
+    got, ref = np.asarray(got, dtype=np.float64), np.asarray(ref, dtype=np.float64)
+    finite = np.isfinite(ref)
+    with np.errstate(invalid="ignore", over="ignore"):
+        near = np.abs(got - np.where(finite, ref, 0.0)) <= tol
+    same = (got == ref) | (np.isnan(got) & np.isnan(ref))
+    return bool(np.where(finite, near, same).all())
