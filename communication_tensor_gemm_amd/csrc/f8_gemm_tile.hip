@@ -22,8 +22,10 @@
 // about 62 KB/us of slabs into LDS and twice that out of it in all of these forms.
 //
 // Precision: as the MX products' E4M3 (mx_gemm_tile.hip): eight consecutive
-// products are added to 2^-13 of the largest one's power of two, 2e-5 of the
-// result's rms, the rest in fp32.
+// products are added to 2^-13 of the largest one's power of two, the rest in fp32.
+// Off from fp64, of the result's rms: normal data 1.5e-5 for any K, one in a hundred
+// columns of K 16 times as loud 3.7e-5 to 7.5e-5 (a loud product cuts the seven beside
+// it).  An fp32 product of the same codes: 1e-7; rounding D to bf16: 1.7e-3.
 #include "f8_common.h"
 #include "mx_tile_loop.h"
 
