@@ -79,12 +79,16 @@ int dist_gemm_f8_dequantize(const void* codes, const void* scales, int64_t rows,
 
 /* The F8 tensor of the transpose (cols x rows) of an F8 tensor (rows x cols):
  * its values, in blocks of 128 along the rows, scaled as by
- * dist_gemm_f8_quantize.  Errors as there. */
+ * dist_gemm_f8_quantize.  The values pass through fp32: one that rounds to 2^128
+ * or more there counts as an infinity, so its block of the transpose is NaN.
+ * (Scale bytes from 247 on can hold such values, of quantised fp32 those that E4M3
+ * rounded up to 2^128: magnitudes from 248 * 2^120 on.)  Errors as there. */
 int dist_gemm_f8_transpose(const void* codes, const void* scales, int64_t rows, int64_t cols, void* codes_t,
                            void* scales_t, void* stream);
 
 /* Bytes of workspace that dist_gemm_f8_product needs on the current device
- * (may be 0; 0 also for sizes it refuses). */
+ * (may be 0; 0 also for sizes it refuses).  Fewer rows may need more: where M
+ * varies, take the largest over the values of M. */
 int64_t dist_gemm_f8_product_workspace(int64_t M, int64_t N, int64_t K);
 
 /* Product of two F8 tensors:
@@ -116,7 +120,7 @@ int dist_gemm_f8_product(const void* A, const void* A_scales, const void* B, con
  *   n = (h - mu) * s, y = n * weight + bias
  * in fp32, y rounded once to what `out` names (the sums too: a row whose sum of
  * squares overflows has s = 0, one whose sum does is NaN, and with eps = 0 a row
- * of equal values has s = infinity and is NaN).  x, residual and h hold `rows`
+ * of equal values has s = infinity and is NaN, one whose squares vanish s = infinity).  x, residual and h hold `rows`
  * rows of `cols` values of `elem`, ldx, ldr and ldh elements apart; weight and
  * bias `cols` values of `elem`, bias may be NULL.  residual and h go together
  * (both NULL or neither); h may be x or residual itself (then with the same
