@@ -9,10 +9,11 @@
 // read once and every output written once, the row staying in registers
 // between its sums and its use.  8192 x 8192 bf16 with residual into F8 with the
 // checkpoint: 95 us, 5.7 TB/s (a copy: 6.2); 4 x 16384 into F8: 5.9 us, the latency
-// of loads, two sums over 16 waves and a store; the gradient of 8192 x 8192 bf16
-// from the checkpoint with dh: 91 us, 5.2 TB/s (its second kernel 6.4 of them), from
-// the stream 100; of 1021 x 5123 fp32 19.7 us, two dependent launches (16.7 and
-// 3.9).
+// of loads one behind another (x; per piece the residual, before h is stored; the
+// weights behind those stores), two sums over 16 waves and a store; the gradient of
+// 8192 x 8192 bf16 from the checkpoint with dh: 91 us, 5.2 TB/s (its second kernel 6.4
+// of them), from the stream 100; of 1021 x 5123 fp32 19.7 us, two dependent launches
+// (16.7 and 3.9), the first one's four rows to a workgroup a memory latency each.
 //
 // The variance is of the differences from a mean, never a difference of two
 // sums: each wave sums its part of the row and the squares around its own
@@ -106,7 +107,8 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(LayerNormArgs a, int W
       }
     }
   }
-  // weight and bias are on their way while the row is summed
+  // (behind the stores of h, which the compiler cannot tell apart from them, and waited for with x before the sums:
+  // loads under branches are not counted)
   Raw8<T> wr[V], br[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) {
@@ -282,12 +284,21 @@ static void norm_out(int out, const LayerNormArgs& a, hipStream_t st) {
 // fixed number of workgroups walks the rows, each keeping its columns' share
 // of dw and db in registers (the row's lanes hold the same columns every
 // time), and writes it out once as a row of `partial`; a second kernel adds
-// those rows.  No atomics: the order of every sum is fixed.  The next row's
-// loads are in flight while the current row's sums cross the waves, where the
-// registers allow it.  Rows of more than 16384 columns have no registers for
-// the columns' sums: there a kernel of its own walks down the columns first
-// (4096 x 32768 bf16 from the checkpoint with dh 272 us, 2048 x 32768 fp32 332: half
-// of the bytes are read twice).
+// those rows.  No atomics: the order of every sum is fixed.
+//
+// The next row's loads are issued before the current row's sums, where the
+// registers allow it (one piece to a lane, and two of bf16).  They hide the row's
+// arithmetic and not much more: the compiler does not count loads under branches,
+// so it waits for all that are under way, in fp32 before the sums cross the waves,
+// at the latest before dx is stored.  A turn then costs a memory latency, which
+// the CU's other workgroups have to cover.  Spills: none with one piece to a lane,
+// nor with two from the stream on aligned rows; from the checkpoint two pieces
+// spill one register of bf16 (11 of unaligned rows) and 11 to 15 of fp32, four
+// pieces up to 50.
+//
+// Rows of more than 16384 columns have no registers for the columns' sums: there a
+// kernel of its own walks down the columns first (4096 x 32768 bf16 from the
+// checkpoint with dh 272 us, 2048 x 32768 fp32 332: half of the bytes are read twice).
 
 // Eight elements of a row's dy and n (or h), as loaded.
 template <int T, bool KEPT>
