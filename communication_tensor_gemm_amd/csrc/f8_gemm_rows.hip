@@ -24,7 +24,7 @@
 //
 // 1 x 13312 x 16384 (220 MB): 38.5 us, 5.7 TB/s, launch and the latency of the
 // first loads included (a copy: 6.2).  More rows of that width, whose A is read
-// again by every workgroup: 4 45 us, 8 52, 16 54, 32 62; 1 x 8192 x 1024 4.2, 16 4.2.
+// again by every workgroup: 4 43 us, 8 49, 16 52, 32 62; 1 x 8192 x 1024 4.2, 16 4.2.
 #include "f8_common.h"
 #include "mx_tiles.h"
 

@@ -13,7 +13,7 @@
 // full.  LDS is the next bound: a slab of a 256 x 256 tile writes 64 KiB into it
 // (64 bytes a cycle) and reads 128 (128 a cycle), as many cycles as its MFMAs.
 // C or a bias beside whole columns: four columns per access (into fp32 with C
-// 238 us, by single elements 280; without C 233).
+// 234 us, by single elements 280; without C 229).
 //
 // Tiles of 64 x 128 (four stages, one workgroup per CU) are for up to one of
 // them per CU: 200 x 8192 x 3584 15 us, 0.38 per slab of 24 KiB; tiles of 128 x 128

@@ -17,8 +17,8 @@
 // (no transposition of bytes), go through LDS, swizzled, and leave as whole
 // lines of 128 bytes.
 //
-// 8192 x 13312 bf16 by rows 54 us, 6.1 TB/s (a copy: 6.2), transposed 57, both
-// 87, 5.0 TB/s; fp32 both 139; back to bf16 57.  Transposing 8192 x 16384 52 us,
+// 8192 x 13312 bf16 by rows 55 us, 6.0 TB/s (a copy: 6.2), transposed 60, both
+// 87, 5.0 TB/s; fp32 by rows 98, both 138; back to bf16 56, to fp32 116.  Transposing 8192 x 16384 52 us,
 // 5.2 TB/s (8192 x 13312 45 us, 4.9): 128-byte pieces of rows on both sides, and
 // single bytes of the scales' lines (without those bytes 4 less).  777 x 3584 by rows 4.1 us, transposed 5.1: a launch's latency.
 #include "f8_common.h"
