@@ -251,20 +251,31 @@ KERNEL_SOURCES = ["communication_tensor_gemm_amd/csrc/distgemm.hip",
 TRAFFIC_FILE = "profiles/fused_run_kernel_hbm_traffic.txt"
 
 
+def _build_flags():
+    """What the kernel sources' units are compiled with, wherever the tree lies: the flags of build.py, which also
+    lists the library's other units."""
+    import runpy
+    build = runpy.run_path(os.path.join(ROOT, KERNEL_SOURCES[-1]))
+    flags = [f.replace(build["ROOT"], "") for f in build["HIPCC_FLAGS"]]
+    units = [os.path.basename(f) for f in KERNEL_SOURCES if f.endswith(".hip")]
+    return "\n".join([*flags, *(f"{u}: {' '.join(build['EXTRA'].get(u, []))}" for u in units)])
+
+
 def kernel_source_hash():
     """Hash of the kernel sources' code: comments, blank lines and trailing
     blanks removed, so that a comment edit leaves a recorded measurement
-    valid and any code change invalidates it."""
+    valid and any code change invalidates it; of build.py, the flags."""
     import hashlib
     import re
     h = hashlib.sha256()
-    for f in KERNEL_SOURCES:
+    for f in KERNEL_SOURCES[:-1]:
         text = open(os.path.join(ROOT, f), encoding="utf-8").read()
         text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
         # // comments (a "//" inside a string literal is not one: the sources have none)
         text = re.sub(r"//[^\n]*", "", text)
         lines = [l.rstrip() for l in text.splitlines()]
         h.update("\n".join(l for l in lines if l).encode())
+    h.update(_build_flags().encode())
     return h.hexdigest()[:16]
 
 
